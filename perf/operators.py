@@ -192,6 +192,14 @@ def _cache(case, lens, g, normal):
     return normal(*shape, dtype=BF16), normal(*shape, dtype=BF16), table
 
 
+def _workspace(s, name, *sizes):
+    """The workspace that a program of the library keeps from call to call."""
+    if own:
+        import long_context_compressed_gated_b200 as csa
+        need = getattr(csa.lib(), name + "_workspace_bytes")(*sizes) if name else 256
+        s["ws"] = torch.zeros(need, dtype=torch.uint8, device="cuda")
+
+
 def prepare(case, seed):
     g, normal = _maker(seed)
     s = {"case": case}
@@ -209,6 +217,7 @@ def prepare(case, seed):
         s["pos"] = torch.arange(T, device="cuda") + case["far"]
         if case["op"] == "norm_rope_grad":
             s["dyq"], s["dyk"] = normal(T, H, d, dtype=ot), normal(T, Hk, d, dtype=ot)
+            _workspace(s, "csa_qk_norm_rope_backward", T, H, Hk, d)
         return s
     if case["op"] == "append":
         new = _appends(case)
@@ -222,6 +231,7 @@ def prepare(case, seed):
             pos.append(torch.full((pad,), -1))
             seq.append(torch.full((n + pad,), b))
         s["pos"], s["seq"] = torch.cat(pos).cuda(), torch.cat(seq).to(torch.int32).cuda()
+        _workspace(s, None)
         return s
     lens, trees = _sequences(case)
     R = sum(map(len, trees))
@@ -240,10 +250,7 @@ def prepare(case, seed):
         s["seq"] = torch.tensor([b for b, t in enumerate(trees) for _ in t], dtype=torch.int32).cuda()
     else:
         s["q"] = normal(R, H, d, dtype=BF16)
-    if own:
-        import long_context_compressed_gated_b200 as csa
-        need = csa.lib().csa_tree_attn_workspace_bytes(case["B"], R, H, Hk, d, case["page"], s["table"].shape[1])
-        s["ws"] = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    _workspace(s, "csa_tree_attn", case["B"], R, H, Hk, d, case["page"], s["table"].shape[1])
     return s
 
 
@@ -365,10 +372,10 @@ def run(s):
                                     out_dtype=TYPES[c["out"]], **rope)
     if c["op"] == "norm_rope_grad":
         return csa.csa_qk_norm_rope_backward(s["q"], s["k"], s["dyq"], s["dyk"], s["inv_freq"], wq=s["wq"],
-                                             wk=s["wk"], pos=s["pos"], **rope)[:4]
+                                             wk=s["wk"], pos=s["pos"], workspace=s["ws"], **rope)[:4]
     if c["op"] == "append":
         csa.csa_paged_append(s["k"], s["v"], s["Kp"], s["Vp"], s["table"], s["seq"], s["pos"], s["inv_freq"],
-                             wk=s["wk"] if c["norm"] else None, **rope)
+                             wk=s["wk"] if c["norm"] else None, workspace=s["ws"], **rope)
         return s["Kp"], s["Vp"]
     scale = 1.0 / math.sqrt(c["d"])
     if c["op"] == "tree":
