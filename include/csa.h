@@ -65,7 +65,8 @@ typedef enum {
   CSA_ERR_CUDA = -4,              /* a CUDA call failed; see csa_last_cuda_error() */
   CSA_ERR_WORKSPACE = -5,         /* workspace null or smaller than required */
   CSA_ERR_DEVICE_TIMEOUT = -6,    /* (status word) a bounded device wait gave up */
-  CSA_ERR_RANGE = -7              /* (status word) MXFP4 scale outside [125,128] */
+  CSA_ERR_RANGE = -7,             /* (status word) MXFP4 scale outside [125,128] */
+  CSA_ERR_INDEX = -8              /* (status word) a sequence, slot or page number outside its table */
 } csa_status_t;
 
 /* Element type of an attention output O (the o_dtype argument). */
@@ -325,6 +326,80 @@ int csa_decode_append(const void* K_new, const void* V_new, const void* Z_new, c
 int hca_decode_append(const void* K_new, const void* V_new, const void* Z_new, const float* Bias, const int64_t* pos,
                       int B, int64_t Ncap, int d, int m, int W, void* Kwin, void* Vwin, void* Kblk, void* Vblk,
                       void* Zblk, void* Kc, void* Vc, csa_stream_t stream);
+
+/* ---------------------------------------------------------------- norm and position rotation
+ * Queries and keys made ready for the attention of this library, which takes
+ * them already positioned (the pages give no positional encoding): per (token,
+ * head) row x of d channels
+ *   RMS norm    n_c = x_c w_c / sqrt(mean_c x_c^2 + eps)   (w = wq / wk [d] f32;
+ *               a NULL weight leaves the norm out: n = x)
+ *   rotation    channel pairs (a, b) of [rot_start, rot_start + rot_dim) turn by
+ *               pos * inv_freq[p]:  y_a = n_a cos - n_b sin, y_b = n_b cos + n_a sin
+ *               CSA_ROPE_HALVES: (a, b) = rot_start + (p, p + rot_dim/2)
+ *               CSA_ROPE_PAIRS : (a, b) = rot_start + (2p, 2p + 1)
+ *               the other channels keep n.
+ *   q [T, H, d], k [T, Hk, d] of element type x_dtype (csa_dtype_t); token rows
+ *          q_stride / k_stride ELEMENTS apart (>= H*d / Hk*d, a multiple of 16
+ *          bytes), so that views of one packed projection are taken as they are;
+ *          H = 0 or Hk = 0 leaves that side out (its pointers are not used)
+ *   pos    [T] int64 DEVICE positions, any value (negative ones too); NULL: t0 + t
+ *   inv_freq  HOST array of rot_dim/2 finite doubles, radians per position, read
+ *          during the call.  Angles are exact in pos (64-bit fractions of a
+ *          turn), so far positions lose nothing.
+ *   yq [T, H, d], yk [T, Hk, d] dense, of element type y_dtype, rounded once.
+ * Sums and the rotation are in fp32.  An output may be its own input (in place)
+ * when the types are equal and the input is dense; any other overlap of outputs
+ * and inputs is CSA_ERR_INVALID_ARG.  d in {64, 128}; rot_dim a multiple of 16
+ * (0: no rotation), rot_start a multiple of 8, rot_start + rot_dim <= d;
+ * H, Hk <= 4096; eps >= 0.  No workspace. */
+enum { CSA_ROPE_HALVES = 0, CSA_ROPE_PAIRS = 1 };
+int csa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const float* wq,
+                     const float* wk, float eps, const int64_t* pos, int64_t t0, const double* inv_freq,
+                     int rot_start, int rot_dim, int rot_style, int64_t T, int H, int Hk, int d, int x_dtype,
+                     void* yq, void* yk, int y_dtype, csa_stream_t stream);
+
+/* Its backward pass.  q, k, weights, positions and rotation as given to the
+ * forward (nothing else is saved: the norms are computed again from x).
+ *   dyq [T, H, d], dyk [T, Hk, d] dense, y_dtype: gradients of yq, yk
+ *   dq, dk of x_dtype: token rows dq_stride / dk_stride elements apart (as q, k)
+ *   dwq, dwk [d] f32 (written, not accumulated; the sums over all tokens and
+ *          heads in a fixed order): given exactly when the side and its weight are
+ * With T = 0 the weight gradients are zeros.  dq / dk must not overlap q, k, dyq
+ * or dyk.  Deterministic on one GPU model (the split of the sums follows its SM
+ * count).  Workspace: csa_qk_norm_rope_backward_workspace_bytes(). */
+size_t csa_qk_norm_rope_backward_workspace_bytes(int64_t T, int H, int Hk, int d);
+int csa_qk_norm_rope_backward(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const float* wq,
+                              const float* wk, float eps, const int64_t* pos, int64_t t0, const double* inv_freq,
+                              int rot_start, int rot_dim, int rot_style, const void* dyq, const void* dyk, int64_t T,
+                              int H, int Hk, int d, int x_dtype, int y_dtype, void* dq, int64_t dq_stride, void* dk,
+                              int64_t dk_stride, float* dwq, float* dwk, void* workspace, size_t workspace_bytes,
+                              csa_stream_t stream);
+
+/* ---------------------------------------------------------------- paged raw cache
+ * New tokens' keys and values into a paged cache of raw (uncompressed) K/V rows,
+ * the keys normed and rotated on the way as by csa_qk_norm_rope (the uncompressed
+ * rows of blog.nickys.cn/?p=150 "1. CSA" / ifanr repost, kept in pages instead of
+ * a shifting window; the pages describe no layout).
+ *   Kpages, Vpages [n_pages, Hk, page, d] bf16; row `slot` of sequence b is row
+ *          slot % page of page block_table[b, slot / page]
+ *   block_table [B, max_pages] int32 DEVICE page numbers
+ *   k, v   [T, Hk, d] bf16, token rows k_stride / v_stride elements apart
+ *   seq    [T] int32 DEVICE: the token's sequence;  slot [T] int64 DEVICE: its row
+ *          (NULL: pos); a negative slot marks a padding row, which is skipped
+ *   pos    [T] int64 DEVICE: the position its key is rotated to (drafted tokens
+ *          of one depth share a position but not a slot)
+ *   wk, eps, inv_freq, rot_*: as csa_qk_norm_rope (wk NULL: no norm)
+ * Rows that no token names keep their bits.  The (sequence, slot) pairs of a call
+ * are distinct.  A sequence, slot or page number outside its table is reported as
+ * CSA_ERR_INDEX in the status word and its token skipped; nothing is read or
+ * written out of bounds.  Tables, slots and positions are read on the device in
+ * stream order, so a captured call follows their new contents.  page a power of
+ * two, 16 .. 256; d in {64, 128}; 1 <= Hk <= 4096.  workspace: >= 256 bytes. */
+int csa_paged_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* wk, float eps,
+                     const int64_t* pos, const int64_t* slot, const int32_t* seq, const double* inv_freq,
+                     int rot_start, int rot_dim, int rot_style, const int32_t* block_table, int64_t T, int Hk, int d,
+                     int B, int max_pages, int64_t n_pages, int page, void* Kpages, void* Vpages, void* workspace,
+                     size_t workspace_bytes, csa_stream_t stream);
 
 /* ---------------------------------------------------------------- decode without allocation
  * csa_decode for callers that cannot allocate device memory: serving loops

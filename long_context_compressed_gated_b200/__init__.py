@@ -17,7 +17,8 @@ __all__ = [
     "CsaError", "lib", "csa_compress", "csa_indexer_topk", "csa_sparse_attn", "hca_attn", "csa_decode",
     "hca_decode", "csa_check_status", "csa_status_string", "csa_version", "LIB_PATH", "csa_decode_append",
     "hca_decode_append", "csa_mxfp4_quantize", "csa_mxfp8_quantize", "csa_decode_fp8", "csa_peak_mma",
-    "csa_decode_search", "csa_topk_merge", "csa_decode_attend", "csa_attn_combine",
+    "csa_decode_search", "csa_topk_merge", "csa_decode_attend", "csa_attn_combine", "rope_inv_freq",
+    "csa_qk_norm_rope", "csa_qk_norm_rope_backward", "csa_paged_append",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libcsa.so")
@@ -70,6 +71,12 @@ def lib():
             "csa_topk_merge": ([P, I, I, I, P, P, P, P, SZ, P], I),
             "csa_decode_attend": ([P, P, P, P, I64, P, P, P, I, I64, I, I, I, I, I, F, P, I, P, P, SZ, P], I),
             "csa_attn_combine": ([P, P, I, I, I, I, P, I, P, P], I),
+            "csa_qk_norm_rope": ([P, I64, P, I64, P, P, F, P, I64, P, I, I, I, I64, I, I, I, I, P, P, I, P], I),
+            "csa_qk_norm_rope_backward_workspace_bytes": ([I64, I, I, I], SZ),
+            "csa_qk_norm_rope_backward": ([P, I64, P, I64, P, P, F, P, I64, P, I, I, I, P, P, I64, I, I, I, I, I, P, I64,
+                                           P, I64, P, P, P, SZ, P], I),
+            "csa_paged_append": ([P, I64, P, I64, P, F, P, P, P, P, I, I, I, P, I64, I, I, I, I, I64, I, P, P, P, SZ,
+                                  P], I),
             "hca_decode": ([P, P, P, P, P, P, I, I64, I, I, I, I, F, P, I, P, P, SZ, P], I),
         }
         for name, (args, res) in sig.items():
@@ -435,3 +442,175 @@ def csa_attn_combine(O_parts, lse_parts, out_dtype=torch.bfloat16, O=None, lse=N
     _check(lib().csa_attn_combine(_ptr(O_parts), _ptr(lse_parts), L, B, H, d, _ptr(O), _ODTYPE[out_dtype], _ptr(lse),
                                   _stream()), "csa_attn_combine")
     return O, lse
+
+
+# ---------------------------------------------------------------- norm, position rotation, paged cache
+ROPE_HALVES, ROPE_PAIRS = 0, 1
+
+
+def rope_inv_freq(rot_dim, base=10000.0):
+    """base^(-2p/rot_dim) for p < rot_dim/2: radians per position of the rotated
+    channel pairs, as a float64 CPU tensor (any other float64 CPU tensor of that
+    length, a stretched or scaled one say, serves as well)."""
+    return float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
+
+
+def _here(*tensors):
+    """Every given tensor is on the current CUDA device."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError("tensors must be on the current CUDA device (cuda:%d), got %s" % (cur, t.device))
+
+
+def _rows(t, dtypes, name):
+    """Token rows [T, heads, d], each row dense: (elements from row to row, heads)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be one of %s, got %s" % (name, dtypes, t.dtype))
+    if t.dim() != 3:
+        raise ValueError("%s must have 3 dims, got %d" % (name, t.dim()))
+    T, heads, d = t.shape
+    rs, hs, cs = t.stride()
+    if T and heads and ((d > 1 and cs != 1) or (heads > 1 and hs != d)):
+        raise ValueError("%s must have dense [heads, d] rows" % name)
+    return (rs if T > 1 else heads * d), heads
+
+
+def _freq(inv_freq):
+    """(host pointer, rot_dim) of the rotation's frequencies; None: no rotation."""
+    if inv_freq is None:
+        return None, 0
+    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq must be a contiguous 1-D float64 CPU tensor")
+    return inv_freq.data_ptr(), 2 * inv_freq.numel()
+
+
+def _weight(w, d, name):
+    if w is not None:
+        _dev(w, torch.float32, name, 1)
+        if w.numel() != d:
+            raise ValueError("%s must have %d elements" % (name, d))
+    return w
+
+
+def _vector(t, n, dtype, name):
+    if t is not None:
+        _dev(t, dtype, name, 1)
+        if t.numel() != n:
+            raise ValueError("%s must have %d elements, got %d" % (name, n, t.numel()))
+    return t
+
+
+def _qk_sides(q, k):
+    if q is None and k is None:
+        raise ValueError("q or k must be given")
+    x = q if q is not None else k
+    qs, H = _rows(q, _ODTYPE, "q") if q is not None else (0, 0)
+    ks, Hk = _rows(k, _ODTYPE, "k") if k is not None else (0, 0)
+    if q is not None and k is not None and (k.dtype != q.dtype or k.shape[0] != q.shape[0] or
+                                            k.shape[2] != q.shape[2]):
+        raise ValueError("q and k must agree in type, tokens and head dim")
+    return x, qs, ks, H, Hk
+
+
+def csa_qk_norm_rope(q, k, inv_freq, wq=None, wk=None, eps=1e-6, pos=None, t0=0, rot_start=0, rot_style=ROPE_HALVES,
+                     yq=None, yk=None, out_dtype=None):
+    """Per-head RMS norm (weights wq/wk [d] f32; None: no norm) and position
+    rotation of queries q [T,H,d] and keys k [T,Hk,d] (bf16 or fp32; views of a
+    packed projection are fine; either may be None).  inv_freq [rot/2] float64 on
+    the CPU (None: no rotation), turning channels rot_start .. rot_start + rot.
+    pos [T] int64 positions on the device, or None: t0, t0 + 1, ...
+    Returns (yq, yk) of out_dtype (default: the inputs' type)."""
+    x, qs, ks, H, Hk = _qk_sides(q, k)
+    T, _, d = x.shape
+    ot = x.dtype if out_dtype is None else out_dtype
+    _weight(wq, d, "wq"), _weight(wk, d, "wk"), _vector(pos, T, torch.int64, "pos")
+    fp, rot = _freq(inv_freq)
+    yq = _out(yq, x, (T, H, d), ot, "yq") if q is not None else None
+    yk = _out(yk, x, (T, Hk, d), ot, "yk") if k is not None else None
+    for y, s, n in ((yq, q, "yq"), (yk, k, "yk")):
+        if y is not None and y.shape != s.shape:
+            raise ValueError("%s must have shape %s" % (n, tuple(s.shape)))
+    _here(q, k, wq, wk, pos, yq, yk)
+    _check(lib().csa_qk_norm_rope(_ptr(q), qs, _ptr(k), ks, _ptr(wq), _ptr(wk), eps, _ptr(pos), t0, fp, rot_start, rot,
+                                  rot_style, T, H, Hk, d, _ODTYPE[x.dtype], _ptr(yq), _ptr(yk), _ODTYPE[ot],
+                                  _stream()), "csa_qk_norm_rope")
+    return yq, yk
+
+
+def csa_qk_norm_rope_backward(q, k, dyq, dyk, inv_freq, wq=None, wk=None, eps=1e-6, pos=None, t0=0, rot_start=0,
+                              rot_style=ROPE_HALVES, dq=None, dk=None, dwq=None, dwk=None, workspace=None):
+    """Gradients of csa_qk_norm_rope from dyq/dyk (the types and shapes of yq/yk):
+    dq/dk of q's type (given ones may be views of a packed gradient), dwq/dwk [d]
+    f32.  Returns (dq, dk, dwq, dwk, workspace), None where there is no input."""
+    x, qs, ks, H, Hk = _qk_sides(q, k)
+    T, _, d = x.shape
+    _weight(wq, d, "wq"), _weight(wk, d, "wk"), _vector(pos, T, torch.int64, "pos")
+    fp, rot = _freq(inv_freq)
+    got = dyq if q is not None else dyk
+    if got is None or got.dtype not in _ODTYPE:
+        raise TypeError("the gradients must be torch.bfloat16 or torch.float32")
+    yt = got.dtype
+    sides = []
+    for s, dy, dx, w, dw, n in ((q, dyq, dq, wq, dwq, "q"), (k, dyk, dk, wk, dwk, "k")):
+        if s is None:
+            if dy is not None or dx is not None or dw is not None:
+                raise ValueError("gradients of %s without %s" % (n, n))
+            sides.append((None, None, 0, None))
+            continue
+        _dev(dy, yt, "dy" + n, 3)
+        dx = torch.empty(s.shape, dtype=s.dtype, device=s.device) if dx is None else dx
+        dxs, _ = _rows(dx, (s.dtype,), "d" + n)
+        if dy.shape != s.shape or dx.shape != s.shape:
+            raise ValueError("dy%s and d%s must have shape %s" % (n, n, tuple(s.shape)))
+        if w is not None:
+            dw = torch.empty(d, dtype=torch.float32, device=s.device) if dw is None else _weight(dw, d, "dw" + n)
+        elif dw is not None:
+            raise ValueError("dw%s without w%s" % (n, n))
+        sides.append((dy, dx, dxs, dw))
+    (dyq, dq, dqs, dwq), (dyk, dk, dks, dwk) = sides
+    L = lib()
+    _here(q, k, wq, wk, pos, dyq, dyk, dq, dk, dwq, dwk, workspace)
+    ws = _workspace(L.csa_qk_norm_rope_backward_workspace_bytes(T, H, Hk, d), x.device, workspace)
+    _check(L.csa_qk_norm_rope_backward(_ptr(q), qs, _ptr(k), ks, _ptr(wq) if H else None, _ptr(wk) if Hk else None,
+                                       eps, _ptr(pos), t0, fp, rot_start, rot, rot_style, _ptr(dyq), _ptr(dyk), T, H,
+                                       Hk, d, _ODTYPE[x.dtype], _ODTYPE[yt], _ptr(dq), dqs, _ptr(dk), dks, _ptr(dwq),
+                                       _ptr(dwk), _ptr(ws), ws.numel(), _stream()), "csa_qk_norm_rope_backward")
+    return dq, dk, dwq, dwk, ws
+
+
+def _paged(Kpages, Vpages, block_table):
+    """(pages, key heads, rows a page, d) of a paged cache."""
+    _dev(Kpages, torch.bfloat16, "Kpages", 4), _dev(Vpages, torch.bfloat16, "Vpages", 4)
+    _dev(block_table, torch.int32, "block_table", 2)
+    if Kpages.shape != Vpages.shape:
+        raise ValueError("Kpages and Vpages must have the same shape")
+    return Kpages.shape
+
+
+def csa_paged_append(k, v, Kpages, Vpages, block_table, seq, pos, inv_freq, slot=None, wk=None, eps=1e-6, rot_start=0,
+                     rot_style=ROPE_HALVES, workspace=None):
+    """Write the tokens' keys (normed by wk [d] f32 unless None, rotated to pos) and
+    values into a paged cache, in place: k, v [T,Hk,d] bf16 (views of a packed
+    projection are fine); Kpages/Vpages [n_pages,Hk,page,d] bf16; block_table
+    [B,max_pages] int32; seq [T] int32; pos, slot [T] int64 on the device (slot
+    None: pos; a negative slot skips its token).  Returns the workspace, whose
+    status word reports numbers outside their tables."""
+    n_pages, Hk, page, d = _paged(Kpages, Vpages, block_table)
+    ks, kh = _rows(k, (torch.bfloat16,), "k")
+    vs, vh = _rows(v, (torch.bfloat16,), "v")
+    T = k.shape[0]
+    if kh != Hk or vh != Hk or k.shape[2] != d or v.shape != k.shape:
+        raise ValueError("k and v must be [T, %d, %d]" % (Hk, d))
+    _vector(seq, T, torch.int32, "seq"), _vector(pos, T, torch.int64, "pos"), _vector(slot, T, torch.int64, "slot")
+    _weight(wk, d, "wk")
+    fp, rot = _freq(inv_freq)
+    _here(k, v, Kpages, Vpages, block_table, seq, pos, slot, wk, workspace)
+    ws = _workspace(256, k.device, workspace)
+    _check(lib().csa_paged_append(_ptr(k), ks, _ptr(v), vs, _ptr(wk), eps, _ptr(pos), _ptr(slot), _ptr(seq), fp,
+                                  rot_start, rot, rot_style, _ptr(block_table), T, Hk, d, block_table.shape[0],
+                                  block_table.shape[1], n_pages, page, _ptr(Kpages), _ptr(Vpages), _ptr(ws),
+                                  ws.numel(), _stream()), "csa_paged_append")
+    return ws

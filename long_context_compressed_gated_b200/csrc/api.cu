@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "attention.cuh"
+#include "checks.cuh"
 #include "common.cuh"
 #include "compress.cuh"
 
@@ -69,8 +70,8 @@ int sm_count() {
 }
 
 namespace {
-
 thread_local int g_last_cuda_error = 0;
+}  // namespace
 
 int cuda_fail(cudaError_t e) {
   g_last_cuda_error = (int)e;
@@ -78,30 +79,10 @@ int cuda_fail(cudaError_t e) {
   return CSA_ERR_CUDA;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-template <typename... P>
-int check_ptrs(P... ps) {
-  const void* arr[] = {static_cast<const void*>(ps)...};
-  for (const void* p : arr) {
-    if (p == nullptr) return CSA_ERR_INVALID_ARG;
-    if (!aligned16(p)) return CSA_ERR_MISALIGNED;
-  }
-  return CSA_OK;
-}
-
-int check_opt(const void* p) { return (p != nullptr && !aligned16(p)) ? CSA_ERR_MISALIGNED : CSA_OK; }
+namespace {
 
 bool valid_H(int H) { return H == 4 || H == 8 || H == 16 || H == 32 || H == 64 || H == 128; }
 bool valid_HI(int HI) { return HI == 4 || HI == 8 || HI == 16 || HI == 32 || HI == 64; }
-
-int check_ws(void* ws, size_t bytes, size_t need) {
-  if (ws == nullptr || bytes < need) return CSA_ERR_WORKSPACE;
-  if (!aligned16(ws)) return CSA_ERR_MISALIGNED;
-  return CSA_OK;
-}
-
-int* status_word(void* ws) { return static_cast<int*>(ws); }
 
 // window tiles a CTA of gq consecutive tokens may need
 int64_t window_tiles(int W, int gq) { return W > 0 ? ceil_div((int64_t)W + gq - 1, 128) : 0; }
@@ -139,9 +120,6 @@ void inline_positions(AttnArgs& a, const int64_t* host, int B) {
   a.npos_in = B;
 }
 
-
-bool valid_odtype(int t) { return t == CSA_BF16 || t == CSA_F32; }
-
 // decode workspace: [header][pos B*8][idx B*k*4][cand B*nsplit*k*8]
 // Key ranges per decode row: as many as fill the GPU in one wave of
 // one-CTA-per-SM indexer blocks (a second partial wave would double the time).
@@ -155,8 +133,6 @@ int decode_nsplit(int B, int64_t Ncap, int k) {
   if (ns > kMaxKeyRanges) ns = kMaxKeyRanges;
   return ns < 1 ? 1 : ns;
 }
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Attention CTAs per decode sequence: enough to fill the GPU, at most one per
 // key tile of the sequence; with more than one, partial outputs go through the
@@ -188,6 +164,7 @@ const char* csa_status_string(int status) {
     case CSA_ERR_WORKSPACE: return "workspace missing or too small";
     case CSA_ERR_DEVICE_TIMEOUT: return "a bounded device-side wait timed out";
     case CSA_ERR_RANGE: return "MXFP4 scale byte outside [125, 128]";
+    case CSA_ERR_INDEX: return "a sequence, slot or page number outside its table";
     default: return "unknown status";
   }
 }

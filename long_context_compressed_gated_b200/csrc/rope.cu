@@ -1,0 +1,393 @@
+// rope.cu - per-head RMS norm of queries and keys with the position rotation, and
+// its backward pass (formulas and thread layout in rope.cuh).
+//
+// Forward, per row:  y_c = r (x_c A_c + x_c' B_c).
+// Backward, from dy: the rotation's transpose first, g = R^T dy, then with
+// xh = x r:  dx = r (g w - xh mean_c(g w xh)),  dw_c = sum over rows of g_c xh_c;
+// without a norm (no weight) dx = g.  r is recomputed from x, which is read
+// anyway, so the forward saves nothing.
+//
+// Bound: HBM.  Forward reads x and writes y once; backward reads x and dy and
+// writes dx.  A group of d/8 lanes takes one token's chunk of heads, so the
+// rotation's coefficients are built once per chunk; the rows of a chunk are
+// loaded kAhead at a time before any is used, to keep enough bytes in flight.
+#include <cmath>
+
+#include "checks.cuh"
+#include "rope.cuh"
+
+namespace csa {
+
+bool rope_params(const double* inv_freq, int rot, RopeParams& p) {
+  constexpr long double kTurn = 6.283185307179586476925286766559L;
+  for (int i = 0; i < rot / 2; ++i) {
+    if (!std::isfinite(inv_freq[i])) return false;
+    const long double t = (long double)inv_freq[i] / kTurn;
+    const long double frac = t - std::floor(t);  // [0, 1)
+    const long double f = std::floor(frac * 18446744073709551616.0L + 0.5L);
+    p.turn[i] = f >= 18446744073709551616.0L ? 0 : (uint64_t)f;
+  }
+  return true;
+}
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kAhead = 4;        // rows of a group loaded before the first is used
+constexpr int kHeadChunk = 16;   // heads of one token that share a set of coefficients
+
+// Queries or keys of one call.
+struct RopeSide {
+  const void *x, *dy;   // x [T, heads, d], token rows x_stride elements apart; dy dense
+  void *y, *dx;         // y dense; dx token rows dx_stride apart
+  const float* w;       // [d], or null: no norm
+  int64_t x_stride, dx_stride;
+  int heads, chunk, chunks;  // heads per unit, units per token
+  int64_t blocks;       // thread blocks of this side
+};
+
+struct RopeArgs {
+  RopeParams p;
+  RopeSide side[2];  // queries, keys
+  int64_t T;
+  float* dw_part;  // backward: [blocks of both sides][d] partial weight gradients
+};
+
+template <int D, typename TX, typename TY, int STYLE>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
+  __shared__ uint64_t s_turn[kRopeMaxPairs];
+  stage_turns(a.p, s_turn);
+  const bool keys = (int64_t)blockIdx.x >= a.side[0].blocks;
+  const RopeSide& sd = a.side[keys];
+  const int64_t unit = ((int64_t)blockIdx.x - (keys ? a.side[0].blocks : 0)) * GROUPS + threadIdx.x / LPR;
+  const int64_t t = unit / sd.chunks;
+  if (t >= a.T) return;
+  const int h0 = (int)(unit % sd.chunks) * sd.chunk;
+  const int n = sd.heads - h0 < sd.chunk ? sd.heads - h0 : sd.chunk;
+  const uint32_t mask = group_mask<D>();
+  const RopeLane rl = rope_lane<D, STYLE>(a.p);
+  using Raw = typename RawOf<TX>::type;
+  const TX* x = static_cast<const TX*>(sd.x) + t * sd.x_stride + (int64_t)h0 * D + 8 * rl.l;
+  TY* y = static_cast<TY*>(sd.y) + (t * sd.heads + h0) * D + 8 * rl.l;
+  Raw raw[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (u < n) load8(x + u * D, raw[u]);
+  float A[8], B[8];
+  {
+    float w[8], wp[8], c[8], s[8];
+    load_weights(sd.w, rl.l, w);
+    load_weights(sd.w, rl.partner % LPR, wp);
+    rope_angles<STYLE>(rl, s_turn, a.p.pos ? a.p.pos[t] : a.p.t0 + t, mask, c, s);
+    rope_coef<STYLE>(rl, c, s, w, wp, A, B);
+  }
+  const bool norm = sd.w != nullptr;
+  for (int h = 0; h < n; h += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (h + u >= n) break;
+      const Raw cur = raw[u];
+      float f[8], o[8];
+      unpack8(cur, f);
+      const float r = norm ? row_rms<D>(f, a.p.eps, mask) : 1.f;
+      rope_row<STYLE>(cur, f, r, A, B, rl.partner, mask, o);
+      if (h + u + kAhead < n) load8(x + (int64_t)(h + u + kAhead) * D, raw[u]);
+      store8(y + (int64_t)(h + u) * D, o);
+    }
+  }
+}
+
+// Backward.  A block's groups take its side's units in turn (block i of the side
+// the units i * GROUPS .., i * GROUPS + blocks * GROUPS .., ...), keep their share
+// of dw in registers, and the block adds its groups' shares in order: one partial
+// row per block, summed in order by norm_rope_dw_kernel (no atomics).
+template <int D, typename TX, typename TY, int STYLE>
+__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
+  __shared__ uint64_t s_turn[kRopeMaxPairs];
+  __shared__ float s_dw[GROUPS * D];
+  stage_turns(a.p, s_turn);
+  const bool keys = (int64_t)blockIdx.x >= a.side[0].blocks;
+  const RopeSide& sd = a.side[keys];
+  const int64_t block = (int64_t)blockIdx.x - (keys ? a.side[0].blocks : 0);
+  const uint32_t mask = group_mask<D>();
+  const RopeLane rl = rope_lane<D, STYLE>(a.p);
+  using RawX = typename RawOf<TX>::type;
+  using RawY = typename RawOf<TY>::type;
+  float w[8], dw[8], one[8];
+  load_weights(sd.w, rl.l, w);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) dw[j] = 0.f, one[j] = 1.f;
+  const bool norm = sd.w != nullptr;
+  const int64_t units = a.T * sd.chunks;
+  for (int64_t unit = block * GROUPS + threadIdx.x / LPR; unit < units; unit += sd.blocks * GROUPS) {
+    const int64_t t = unit / sd.chunks;
+    const int h0 = (int)(unit % sd.chunks) * sd.chunk;
+    const int n = sd.heads - h0 < sd.chunk ? sd.heads - h0 : sd.chunk;
+    const TX* x = static_cast<const TX*>(sd.x) + t * sd.x_stride + (int64_t)h0 * D + 8 * rl.l;
+    const TY* dy = static_cast<const TY*>(sd.dy) + (t * sd.heads + h0) * D + 8 * rl.l;
+    TX* dx = static_cast<TX*>(sd.dx) + t * sd.dx_stride + (int64_t)h0 * D + 8 * rl.l;
+    constexpr int AHEAD = 2;
+    RawX rx[AHEAD];
+    RawY ry[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (u < n) load8(x + u * D, rx[u]), load8(dy + u * D, ry[u]);
+    float A[8], B[8];
+    {
+      float c[8], s[8];
+      rope_angles<STYLE>(rl, s_turn, a.p.pos ? a.p.pos[t] : a.p.t0 + t, mask, c, s);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] = -s[j];  // the transpose turns back
+      rope_coef<STYLE>(rl, c, s, one, one, A, B);
+    }
+    for (int h = 0; h < n; h += AHEAD) {
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        if (h + u >= n) break;
+        const RawX cx = rx[u];
+        const RawY cy = ry[u];
+        if (h + u + AHEAD < n) {
+          load8(x + (int64_t)(h + u + AHEAD) * D, rx[u]);
+          load8(dy + (int64_t)(h + u + AHEAD) * D, ry[u]);
+        }
+        float f[8], e[8], g[8];
+        unpack8(cx, f);
+        unpack8(cy, e);
+        rope_row<STYLE>(cy, e, 1.f, A, B, rl.partner, mask, g);
+        if (norm) {
+          float q = 0.f, v = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) q = fmaf(f[j], f[j], q), v = fmaf(g[j] * w[j], f[j], v);
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) {
+            q += __shfl_xor_sync(mask, q, o);
+            v += __shfl_xor_sync(mask, v, o);
+          }
+          const float r = rsqrtf(q * (1.0f / D) + a.p.eps);
+          const float k = v * (1.0f / D) * r * r;  // x k = xh mean(g w xh)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            dw[j] = fmaf(g[j], f[j] * r, dw[j]);
+            g[j] = r * fmaf(-f[j], k, g[j] * w[j]);
+          }
+        }
+        store8(dx + (int64_t)(h + u) * D, g);
+      }
+    }
+  }
+  if (!norm) return;
+  const int grp = threadIdx.x / LPR;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s_dw[grp * D + 8 * rl.l + j] = dw[j];
+  __syncthreads();
+  if ((int)threadIdx.x < D) {
+    float sum = 0.f;
+    for (int i = 0; i < GROUPS; ++i) sum += s_dw[i * D + threadIdx.x];
+    a.dw_part[(int64_t)blockIdx.x * D + threadIdx.x] = sum;
+  }
+}
+
+// dw = sum of a side's partial rows: block 0 the queries', block 1 the keys';
+// 8 threads per channel take every eighth row, then add up in order.
+template <int D>
+__global__ void __launch_bounds__(8 * D) norm_rope_dw_kernel(const float* part, int64_t qblocks, int64_t kblocks,
+                                                             float* dwq, float* dwk) {
+  griddep_wait();
+  float* dw = blockIdx.x ? dwk : dwq;
+  if (dw == nullptr) return;
+  const int64_t n = blockIdx.x ? kblocks : qblocks;
+  const float* p = part + (blockIdx.x ? qblocks * D : 0);
+  __shared__ float s[8 * D];
+  const int c = threadIdx.x % D, g = threadIdx.x / D;
+  float sum = 0.f;
+#pragma unroll 8
+  for (int64_t i = g; i < n; i += 8) sum += p[i * D + c];
+  s[g * D + c] = sum;
+  __syncthreads();
+  if (g == 0) {
+    for (int i = 1; i < 8; ++i) sum += s[i * D + c];
+    dw[c] = sum;
+  }
+}
+
+// Thread blocks that one pass over a side takes.
+int64_t side_blocks(int64_t T, int heads, int d) {
+  return ceil_div(T * ceil_div(heads, kHeadChunk), kThreads / (d / 8));
+}
+
+// Backward: at most this many blocks (their partial rows of dw are summed by one
+// block), four per SM.
+int64_t bwd_blocks(int64_t T, int heads, int d) {
+  const int64_t n = side_blocks(T, heads, d), most = 4 * (int64_t)sm_count();
+  return n < most ? n : most;
+}
+
+void fill_side(RopeSide& s, int heads) {
+  s.heads = heads;
+  s.chunk = heads < kHeadChunk ? heads : kHeadChunk;
+  s.chunks = heads > 0 ? (int)ceil_div(heads, kHeadChunk) : 1;
+}
+
+template <int D, typename TX, typename TY, int STYLE>
+cudaError_t launch_one(const RopeArgs& a, bool bwd, cudaStream_t stream) {
+  const int64_t grid = a.side[0].blocks + a.side[1].blocks;
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  return launch_kernel(bwd ? norm_rope_bwd_kernel<D, TX, TY, STYLE> : norm_rope_kernel<D, TX, TY, STYLE>,
+                       dim3((unsigned)grid), dim3(kThreads), 0, stream, false, a);
+}
+
+template <int D>
+cudaError_t launch_types(const RopeArgs& a, int xt, int yt, bool bwd, cudaStream_t stream) {
+  using bf = __nv_bfloat16;
+  const bool halves = a.p.style == CSA_ROPE_HALVES;
+#define CSA_GO(TX, TY)                                                                   \
+  (halves ? launch_one<D, TX, TY, CSA_ROPE_HALVES>(a, bwd, stream)                       \
+          : launch_one<D, TX, TY, CSA_ROPE_PAIRS>(a, bwd, stream))
+  if (xt == CSA_BF16) return yt == CSA_BF16 ? CSA_GO(bf, bf) : CSA_GO(bf, float);
+  return yt == CSA_BF16 ? CSA_GO(float, bf) : CSA_GO(float, float);
+#undef CSA_GO
+}
+
+// Arguments that forward and backward share.
+int check_rope(int64_t T, int H, int Hk, int d, int x_dtype, int y_dtype, const void* q, int64_t q_stride,
+               const void* k, int64_t k_stride, const float* wq, const float* wk, float eps,
+               const double* inv_freq, int rot_start, int rot_dim, int rot_style, RopeArgs& a) {
+  if (T < 0 || H < 0 || Hk < 0 || H > 4096 || Hk > 4096 || !valid_odtype(x_dtype) || !valid_odtype(y_dtype))
+    return CSA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return CSA_ERR_UNSUPPORTED_SHAPE;
+  const int unit = x_dtype == CSA_BF16 ? 8 : 4;  // elements of 16 bytes
+  if (H > 0 && (q_stride < (int64_t)H * d || q_stride % unit != 0)) return CSA_ERR_INVALID_ARG;
+  if (Hk > 0 && (k_stride < (int64_t)Hk * d || k_stride % unit != 0)) return CSA_ERR_INVALID_ARG;
+  int rc = check_rotation(d, inv_freq, rot_start, rot_dim, rot_style, eps);
+  if (rc) return rc;
+  if (T > 0 && H > 0 && (rc = check_ptrs(q))) return rc;
+  if (T > 0 && Hk > 0 && (rc = check_ptrs(k))) return rc;
+  if ((rc = check_opt(wq)) || (rc = check_opt(wk))) return rc;
+  if (!rope_params(inv_freq, rot_dim, a.p)) return CSA_ERR_INVALID_ARG;
+  a.p.start = rot_start;
+  a.p.rot = rot_dim;
+  a.p.style = rot_style;
+  a.p.eps = eps;
+  a.T = T;
+  fill_side(a.side[0], H);
+  fill_side(a.side[1], Hk);
+  a.side[0].x = q, a.side[0].x_stride = q_stride, a.side[0].w = wq;
+  a.side[1].x = k, a.side[1].x_stride = k_stride, a.side[1].w = wk;
+  return CSA_OK;
+}
+
+}  // namespace
+
+int check_rotation(int d, const double* inv_freq, int rot_start, int rot_dim, int rot_style, float eps) {
+  if ((rot_style != CSA_ROPE_HALVES && rot_style != CSA_ROPE_PAIRS) || !(std::isfinite(eps) && eps >= 0.f))
+    return CSA_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim % 16 != 0 || rot_start < 0 || rot_start % 8 != 0 || rot_start + rot_dim > d)
+    return CSA_ERR_UNSUPPORTED_SHAPE;
+  return rot_dim > 0 && inv_freq == nullptr ? CSA_ERR_INVALID_ARG : CSA_OK;
+}
+
+}  // namespace csa
+
+using namespace csa;
+
+extern "C" {
+
+int csa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const float* wq,
+                     const float* wk, float eps, const int64_t* pos, int64_t t0, const double* inv_freq,
+                     int rot_start, int rot_dim, int rot_style, int64_t T, int H, int Hk, int d, int x_dtype,
+                     void* yq, void* yk, int y_dtype, csa_stream_t stream) {
+  RopeArgs a{};
+  int rc = check_rope(T, H, Hk, d, x_dtype, y_dtype, q, q_stride, k, k_stride, wq, wk, eps, inv_freq, rot_start,
+                      rot_dim, rot_style, a);
+  if (rc) return rc;
+  if ((rc = check_opt(pos))) return rc;
+  if (T == 0 || (H == 0 && Hk == 0)) return CSA_OK;
+  if (H > 0 && (rc = check_ptrs(yq))) return rc;
+  if (Hk > 0 && (rc = check_ptrs(yk))) return rc;
+  // in place is fine (a row's lanes read it before they write it); any other overlap is not
+  const int heads[2] = {H, Hk};
+  void* out[2] = {yq, yk};
+  for (int i = 0; i < 2; ++i) {
+    const size_t on = span(T, (int64_t)heads[i] * d, heads[i], d, y_dtype);
+    for (int j = 0; j < 2; ++j) {
+      const RopeSide& s = a.side[j];
+      const bool in_place = i == j && out[i] == s.x && x_dtype == y_dtype && s.x_stride == (int64_t)s.heads * d;
+      if (!in_place && overlap(out[i], on, s.x, span(T, s.x_stride, s.heads, d, x_dtype))) return CSA_ERR_INVALID_ARG;
+    }
+    a.side[i].y = out[i];
+    a.side[i].blocks = heads[i] > 0 ? side_blocks(T, heads[i], d) : 0;
+  }
+  if (overlap(yq, span(T, (int64_t)H * d, H, d, y_dtype), yk, span(T, (int64_t)Hk * d, Hk, d, y_dtype)))
+    return CSA_ERR_INVALID_ARG;
+  a.p.pos = pos;
+  a.p.t0 = t0;
+  cudaError_t e = d == 128 ? launch_types<128>(a, x_dtype, y_dtype, false, (cudaStream_t)stream)
+                           : launch_types<64>(a, x_dtype, y_dtype, false, (cudaStream_t)stream);
+  return e == cudaSuccess ? CSA_OK : cuda_fail(e);
+}
+
+size_t csa_qk_norm_rope_backward_workspace_bytes(int64_t T, int H, int Hk, int d) {
+  if (T <= 0 || d <= 0) return kWorkspaceHeader;
+  const int64_t rows = (H > 0 ? bwd_blocks(T, H, d) : 0) + (Hk > 0 ? bwd_blocks(T, Hk, d) : 0);
+  return kWorkspaceHeader + align256((size_t)rows * d * 4);
+}
+
+int csa_qk_norm_rope_backward(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const float* wq,
+                              const float* wk, float eps, const int64_t* pos, int64_t t0, const double* inv_freq,
+                              int rot_start, int rot_dim, int rot_style, const void* dyq, const void* dyk, int64_t T,
+                              int H, int Hk, int d, int x_dtype, int y_dtype, void* dq, int64_t dq_stride, void* dk,
+                              int64_t dk_stride, float* dwq, float* dwk, void* workspace, size_t workspace_bytes,
+                              csa_stream_t stream) {
+  RopeArgs a{};
+  int rc = check_rope(T, H, Hk, d, x_dtype, y_dtype, q, q_stride, k, k_stride, wq, wk, eps, inv_freq, rot_start,
+                      rot_dim, rot_style, a);
+  if (rc) return rc;
+  if ((rc = check_opt(pos))) return rc;
+  if ((H > 0 && wq != nullptr) != (dwq != nullptr) || (Hk > 0 && wk != nullptr) != (dwk != nullptr))
+    return CSA_ERR_INVALID_ARG;
+  if ((rc = check_opt(dwq)) || (rc = check_opt(dwk))) return rc;
+  const int heads[2] = {H, Hk};
+  const void* dy[2] = {dyq, dyk};
+  void* dx[2] = {dq, dk};
+  const int64_t dxs[2] = {dq_stride, dk_stride};
+  const int unit = x_dtype == CSA_BF16 ? 8 : 4;
+  for (int i = 0; i < 2; ++i)
+    if (heads[i] > 0 && (dxs[i] < (int64_t)heads[i] * d || dxs[i] % unit != 0)) return CSA_ERR_INVALID_ARG;
+  rc = check_ws(workspace, workspace_bytes, csa_qk_norm_rope_backward_workspace_bytes(T, H, Hk, d));
+  if (rc) return rc;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (T == 0) {  // no rows: the weight gradients are empty sums
+    cudaError_t e = cudaSuccess;
+    for (float* dw : {dwq, dwk})
+      if (dw != nullptr && e == cudaSuccess) e = cudaMemsetAsync(dw, 0, (size_t)d * 4, s);
+    return e == cudaSuccess ? CSA_OK : cuda_fail(e);
+  }
+  if (H == 0 && Hk == 0) return CSA_OK;
+  for (int i = 0; i < 2; ++i) {
+    if (heads[i] == 0) continue;
+    if ((rc = check_ptrs(dy[i], dx[i]))) return rc;
+    for (int j = 0; j < 2; ++j) {
+      const size_t dn = span(T, dxs[i], heads[i], d, x_dtype);
+      if (overlap(dx[i], dn, a.side[j].x, span(T, a.side[j].x_stride, heads[j], d, x_dtype)) ||
+          overlap(dx[i], dn, dy[j], span(T, (int64_t)heads[j] * d, heads[j], d, y_dtype)))
+        return CSA_ERR_INVALID_ARG;
+    }
+    a.side[i].dy = dy[i];
+    a.side[i].dx = dx[i];
+    a.side[i].dx_stride = dxs[i];
+    a.side[i].blocks = bwd_blocks(T, heads[i], d);
+  }
+  a.p.pos = pos;
+  a.p.t0 = t0;
+  a.dw_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceHeader);
+  cudaError_t e = d == 128 ? launch_types<128>(a, x_dtype, y_dtype, true, s)
+                           : launch_types<64>(a, x_dtype, y_dtype, true, s);
+  if (e == cudaSuccess && (dwq || dwk))
+    e = launch_kernel(d == 128 ? norm_rope_dw_kernel<128> : norm_rope_dw_kernel<64>, dim3(2), dim3(8 * d), 0, s, true,
+                      (const float*)a.dw_part, a.side[0].blocks, a.side[1].blocks, dwq, dwk);
+  return e == cudaSuccess ? CSA_OK : cuda_fail(e);
+}
+
+}  // extern "C"
