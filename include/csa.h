@@ -401,6 +401,43 @@ int csa_paged_append(const void* k, int64_t k_stride, const void* v, int64_t v_s
                      int B, int max_pages, int64_t n_pages, int page, void* Kpages, void* Vpages, void* workspace,
                      size_t workspace_bytes, csa_stream_t stream);
 
+/* Attention of drafted tokens over that cache: the decode case for one or several
+ * tokens per sequence, a tree of drafts among them (one token with mask 1 is
+ * plain decode).  Rows q_start[b] .. q_start[b+1]-1 of the call are the nodes of
+ * sequence b; node i is the cache row seq_lens[b] + i, which csa_paged_append has
+ * written, behind the seq_lens[b] committed rows.  Row r sees
+ *   - the committed rows s < seq_lens[b], with W >= 0 only those with
+ *     s > pos[r] - W (W = -1: all of them);
+ *   - the drafted rows seq_lens[b] + j whose bit j is set in mask[r] (its
+ *     ancestors and itself, for a tree; bits of nodes that are not there are
+ *     ignored; the window does not bound drafted rows).
+ *   q      [R, H, d] bf16 (positioned); query head h reads key head h / (H/Hk)
+ *   Kpages, Vpages, block_table: as csa_paged_append.  Entries of a table that
+ *          no visible row needs are not read (freed or -1 pages may stand there)
+ *   seq_lens [B], q_start [B+1] int32 DEVICE; q_start does not decrease, stays in
+ *          [0, R], and a sequence has at most 64 nodes (none is fine)
+ *   mask   [R] uint64 DEVICE;  pos [R] int64 DEVICE (may be NULL when W = -1)
+ *   O      [R, H, d] of element type o_dtype;  lse [R, H] float (nullable), as in
+ *          csa_sparse_attn: partial results for csa_attn_combine, say with a
+ *          csa_sparse_attn over compressed entries (both with CSA_F32 outputs)
+ * A row that sees nothing gets O = 0, lse = -inf.  Rows outside every sequence are
+ * left as they were.  Cache rows that no row of their sequence sees may hold
+ * anything, infinities and NaN included; those that some row sees hold finite
+ * values.  The softmax weights are rounded to bf16 for the product with V (also
+ * with an fp32 output); sums and statistics are fp32.
+ * A length, node count or page number outside its bounds is reported as
+ * CSA_ERR_INDEX in the status word, nothing is read or written out of bounds and
+ * the rows of that sequence are unspecified.  All of it is read on the device in
+ * stream order, so a captured call follows new lengths, tables and masks.
+ * d in {64, 128}; page as csa_paged_append; H <= 1024, H % Hk == 0, any ratio;
+ * max_pages * page < 2^31.  Workspace: csa_tree_attn_workspace_bytes(); calls that
+ * can overlap on the GPU need one each. */
+size_t csa_tree_attn_workspace_bytes(int B, int64_t R, int H, int Hk, int d, int page, int max_pages);
+int csa_tree_attn(const void* q, const void* Kpages, const void* Vpages, const int32_t* block_table,
+                  const int32_t* seq_lens, const int32_t* q_start, const uint64_t* mask, const int64_t* pos, int64_t R,
+                  int B, int H, int Hk, int d, int page, int64_t n_pages, int max_pages, int W, float scale, void* O,
+                  int o_dtype, float* lse, void* workspace, size_t workspace_bytes, csa_stream_t stream);
+
 /* ---------------------------------------------------------------- decode without allocation
  * csa_decode for callers that cannot allocate device memory: serving loops
  * that forbid allocator calls once they are running, embedders that own every

@@ -18,7 +18,7 @@ __all__ = [
     "hca_decode", "csa_check_status", "csa_status_string", "csa_version", "LIB_PATH", "csa_decode_append",
     "hca_decode_append", "csa_mxfp4_quantize", "csa_mxfp8_quantize", "csa_decode_fp8", "csa_peak_mma",
     "csa_decode_search", "csa_topk_merge", "csa_decode_attend", "csa_attn_combine", "rope_inv_freq",
-    "csa_qk_norm_rope", "csa_qk_norm_rope_backward", "csa_paged_append",
+    "csa_qk_norm_rope", "csa_qk_norm_rope_backward", "csa_paged_append", "csa_tree_attn",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libcsa.so")
@@ -77,6 +77,8 @@ def lib():
                                            P, I64, P, P, P, SZ, P], I),
             "csa_paged_append": ([P, I64, P, I64, P, F, P, P, P, P, I, I, I, P, I64, I, I, I, I, I64, I, P, P, P, SZ,
                                   P], I),
+            "csa_tree_attn_workspace_bytes": ([I, I64, I, I, I, I, I], SZ),
+            "csa_tree_attn": ([P, P, P, P, P, P, P, P, I64, I, I, I, I, I, I64, I, I, F, P, I, P, P, SZ, P], I),
             "hca_decode": ([P, P, P, P, P, P, I, I64, I, I, I, I, F, P, I, P, P, SZ, P], I),
         }
         for name, (args, res) in sig.items():
@@ -614,3 +616,36 @@ def csa_paged_append(k, v, Kpages, Vpages, block_table, seq, pos, inv_freq, slot
                                   block_table.shape[1], n_pages, page, _ptr(Kpages), _ptr(Vpages), _ptr(ws),
                                   ws.numel(), _stream()), "csa_paged_append")
     return ws
+
+
+def csa_tree_attn(q, Kpages, Vpages, block_table, seq_lens, q_start, mask, scale, W=-1, pos=None, O=None, lse=None,
+                  want_lse=True, workspace=None, out_dtype=torch.bfloat16):
+    """Attention of drafted tokens (or of one token a sequence) over a paged cache:
+    q [R,H,d] bf16, the rows q_start[b] .. q_start[b+1] of it the nodes of sequence
+    b, whose cache rows follow its seq_lens[b] committed ones; mask [R] int64
+    (storage of the uint64 bits): the drafted rows of its own sequence that a row
+    sees; W >= 0: committed rows s > pos[r] - W only.  Returns (O, lse, workspace)."""
+    n_pages, Hk, page, d = _paged(Kpages, Vpages, block_table)
+    _dev(q, torch.bfloat16, "q", 3)
+    R, H, dq = q.shape
+    if dq != d:
+        raise ValueError("q must have head dim %d, got %d" % (d, dq))
+    B, max_pages = block_table.shape
+    _vector(seq_lens, B, torch.int32, "seq_lens"), _vector(q_start, B + 1, torch.int32, "q_start")
+    _vector(mask, R, torch.int64, "mask"), _vector(pos, R, torch.int64, "pos")
+    O = _out(O, q, q.shape, out_dtype)
+    if O.shape != q.shape:
+        raise ValueError("O must have shape %s" % (tuple(q.shape),))
+    if lse is not None:
+        _dev(lse, torch.float32, "lse", 2)
+        if lse.shape != (R, H):
+            raise ValueError("lse must have shape (%d, %d)" % (R, H))
+    elif want_lse:
+        lse = torch.empty(R, H, dtype=torch.float32, device=q.device)
+    L = lib()
+    _here(q, Kpages, Vpages, block_table, seq_lens, q_start, mask, pos, O, lse, workspace)
+    ws = _workspace(L.csa_tree_attn_workspace_bytes(B, R, H, Hk, d, page, max_pages), q.device, workspace)
+    _check(L.csa_tree_attn(_ptr(q), _ptr(Kpages), _ptr(Vpages), _ptr(block_table), _ptr(seq_lens), _ptr(q_start),
+                           _ptr(mask), _ptr(pos), R, B, H, Hk, d, page, n_pages, max_pages, W, scale, _ptr(O),
+                           _ODTYPE[out_dtype], _ptr(lse), _ptr(ws), ws.numel(), _stream()), "csa_tree_attn")
+    return O, lse, ws

@@ -89,6 +89,24 @@ def test_paged_append_refuses(lib, change, code):
     assert lib.csa_paged_append(*a.values()) == code
 
 
+TREE = dict(q=A[0], Kp=A[1], Vp=A[2], table=A[3], lens=A[4], start=A[5], mask=A[6], pos=A[7], R=10, B=3, H=8, Hk=2,
+            d=64, page=16, n_pages=12, max_pages=4, W=-1, scale=0.1, O=A[8], ot=0, lse=A[9], ws=A[10], wsb=1 << 30,
+            stream=None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(R=-1), INV), (dict(R=1 << 31), INV), (dict(B=-1), INV), (dict(H=0), INV), (dict(Hk=0), INV),
+    (dict(n_pages=-1), INV), (dict(max_pages=-1), INV), (dict(W=-2), INV), (dict(scale=0.0), INV),
+    (dict(scale=float("inf")), INV), (dict(scale=float("nan")), INV), (dict(ot=2), INV), (dict(d=256), SHAPE),
+    (dict(page=24), SHAPE), (dict(H=2048), SHAPE), (dict(Hk=3), SHAPE), (dict(max_pages=1 << 27), SHAPE),
+    (dict(ws=None), WS), (dict(wsb=16), WS), (dict(ws=ODD), MIS), (dict(q=None), INV), (dict(Kp=None), INV),
+    (dict(Vp=ODD), MIS), (dict(table=None), INV), (dict(lens=None), INV), (dict(start=ODD), MIS), (dict(mask=None), INV),
+    (dict(W=4, pos=None), INV), (dict(O=None), INV), (dict(lse=ODD), MIS), (dict(R=0), 0), (dict(B=0), 0)])
+def test_tree_attn_refuses(lib, change, code):
+    a = dict(TREE, **change)
+    assert lib.csa_tree_attn(*a.values()) == code
+
+
 def test_binding_refuses_host_tensors():
     import long_context_compressed_gated_b200 as csa
     q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
