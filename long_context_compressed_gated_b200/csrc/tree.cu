@@ -5,85 +5,850 @@
 // bit j its mask holds; one softmax over both:
 //   O = sum_s p_s v_s,  p_s = exp(scale q.k_s - lse),  lse = log sum_s exp(scale q.k_s).
 // One token per sequence with mask 1 is ordinary decode over the cache.
+//
+// Work.  The rows of one (sequence, key head) are its nodes times the G = H/Hk
+// query heads that share the key head, 128 to a tensor tile (TMEM lane = row).
+// Up to 256 rows make one item, which walks the keys of its sequence in tiles of
+// 128 from the first one that any row sees.  All items' key tiles form one line,
+// cut into equal shares, one per CTA (one CTA per SM, persistent): lengths may be
+// as ragged as they like.  A share that covers an item only in part writes an
+// fp32 partial (O, lse); tree_combine_kernel merges those.  Lengths are read on
+// the device, so the cut follows them in a captured graph.
+//
+// One CTA:
+//   warps 0..3, 4..7  two softmax streams, one thread per row;
+//   warp 8            walks the share, publishes its segments, fetches K and V
+//                     pages by TMA (one box per page and 64 channels);
+//   warp 9            TMEM and MMA issue.
+// An item of more than 128 rows gives each stream one row tile, and both use
+// every K/V tile; a smaller item gives both streams the same rows and alternate
+// key tiles.  Either way one stream's softmax runs while the tensor pipe works on
+// the other's tile.  Per stream and key tile: S = Q K^T (tcgen05, fp32 in TMEM),
+// online softmax with the whole row in one thread's registers, P as bf16 back
+// over S's columns, O += P V with A = P from TMEM.  The tensor pipe runs one
+// thread's products in the order of issue, so S of a stream's next tile may be
+// issued right behind the PV that reads the P in the same columns, and a
+// completed S means that the PV before it is complete too: the accumulator can be
+// rescaled without a further wait.
+//
+// Masks: whole tiles below every row's window are never fetched; in the others a
+// row's visible columns are four 32-bit words (committed range, shifted draft
+// mask), built only for tiles that some row sees in part.  K outside is masked
+// after the product (selected, never added, so NaN there does nothing); V rows
+// that no row of the sequence sees are zeroed in shared memory before the
+// product, since 0 * NaN would not be 0.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <cmath>
 
 #include "checks.cuh"
+#include "sm100.cuh"
 
 namespace csa {
 
+using namespace sm100;
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn get_encode_fn();
+
 namespace {
 
+constexpr int kTile = 128;          // rows of a tensor tile, keys of a key tile
+constexpr int kItemRows = 2 * kTile;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 384;       // three warpgroups (the last two warps idle)
+// Registers: 384 threads launch with 168 each; the softmax groups, which hold a
+// row of S, take 208 and the third group keeps 88 (2 * 208 + 88 = 3 * 168).
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kMaxNodes = 64;       // bits of a mask
+constexpr int kMinShare = 8;        // key tiles a CTA takes at least
+constexpr float kRescaleSlack = 8.0f;  // raise the running max only when it grows by > 2^8
+constexpr float kLn2 = 0.69314718055994531f;
+
+struct alignas(64) TreeMaps {
+  CUtensorMap k, v;
+};
+
 struct TreeArgs {
-  const __nv_bfloat16 *q, *Kp, *Vp;
+  const __nv_bfloat16* q;
   const int32_t *table, *lens, *q_start;
   const uint64_t* mask;
   const int64_t* pos;
   int64_t R, n_pages;
-  int B, H, Hk, max_pages, page_shift, W;
+  int B, H, Hk, G, max_pages, page_shift, W;
   float scale_log2;
   void* O;
   int o_f32;
   float* lse;
   int* status;
+  // partial results of shares that cover an item in part: slot 2c the first
+  // segment of CTA c, 2c+1 its last; [slots][part_rows][D] and [slots][part_rows]
+  float *part_o, *part_lse;
+  int part_rows;
+  int4* split;  // [grid]: the item that CTA c starts and does not finish (see tree_combine_kernel)
 };
 
-// One warp per (row, head): lanes own d/32 channels, the running maximum and sum
-// of the softmax in fp32.
-template <int D>
-__global__ void __launch_bounds__(128) tree_attn_kernel(const __grid_constant__ TreeArgs a) {
-  constexpr int C = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int64_t r = w / a.H;
-  const int h = (int)(w % a.H);
-  if (r >= a.R) return;
-  int b = -1;
-  for (int i = 0; i < a.B; ++i) {
-    const int64_t r0 = a.q_start[i], r1 = a.q_start[i + 1];
-    if (r0 < 0 || r1 < r0 || r1 > a.R) report(a.status, CSA_ERR_INDEX);
-    else if (r0 <= r && r < r1) b = i;
+// What one sequence asks for.
+struct Seq {
+  int r0, n;        // first row of the call, nodes
+  int64_t L, S;     // committed rows, all rows
+  int64_t lo;       // first row that any node may see
+  int64_t tile0;    // first key tile
+  int tiles;        // key tiles (one at least: an item without keys still writes its rows)
+  int sets;         // items per key head: ceil(n * G / 256)
+  __device__ int64_t total(int Hk) const { return (int64_t)tiles * sets * Hk; }
+};
+
+// 2^x with the SFU (ex2.approx, ~2 ulp; -inf -> +0).
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b, bool tell) {
+  Seq q;
+  q.r0 = a.q_start[b];
+  const int r1 = a.q_start[b + 1];
+  q.L = a.lens[b];
+  q.n = r1 - q.r0;
+  q.S = q.L + q.n;
+  q.lo = 0;
+  if (q.r0 < 0 || q.n < 0 || r1 > a.R || q.L < 0 || q.n > kMaxNodes || q.S > ((int64_t)a.max_pages << a.page_shift)) {
+    if (tell) report(a.status, CSA_ERR_INDEX);
+    q.n = 0;
   }
-  if (b < 0) return;  // behind the last sequence
-  const int64_t L = a.lens[b];
-  const int n = a.q_start[b + 1] - a.q_start[b];
-  if (L < 0 || n > 64 || L + n > ((int64_t)a.max_pages << a.page_shift)) {
-    report(a.status, CSA_ERR_INDEX);
-    return;
+  if (q.n == 0) {
+    q.tiles = q.sets = 0;
+    q.tile0 = 0;
+    return q;
   }
-  const uint64_t mask = a.mask[r];
-  const int hk = h / (a.H / a.Hk);
-  float q[C], o[C];
-  for (int c = 0; c < C; ++c) q[c] = __bfloat162float(a.q[(r * a.H + h) * D + lane * C + c]), o[c] = 0.f;
-  int64_t lo = 0;
   if (a.W >= 0) {
-    lo = a.pos[r] - a.W + 1;
-    lo = lo < 0 ? 0 : lo > L ? L : lo;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int64_t s = lo; s < L + n; ++s) {
-    if (s >= L && !(mask >> (s - L) & 1)) continue;
-    const int64_t page = a.table[(int64_t)b * a.max_pages + (s >> a.page_shift)];
-    if (page < 0 || page >= a.n_pages) {
-      report(a.status, CSA_ERR_INDEX);
-      continue;
+    int64_t p = a.pos[q.r0];
+#pragma unroll 8
+    for (int i = 1; i < q.n; ++i) {
+      const int64_t x = a.pos[q.r0 + i];
+      p = x < p ? x : p;
     }
-    const int64_t at = (((page * a.Hk + hk) << a.page_shift) + (s & ((1 << a.page_shift) - 1))) * D + lane * C;
-    float z = 0.f;
-    for (int c = 0; c < C; ++c) z = fmaf(q[c], __bfloat162float(a.Kp[at + c]), z);
-    for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-    z *= a.scale_log2;
-    const float mn = fmaxf(m, z), f = exp2f(m - mn), p = exp2f(z - mn);
-    l = l * f + p;
-    for (int c = 0; c < C; ++c) o[c] = o[c] * f + p * __bfloat162float(a.Vp[at + c]);
-    m = mn;
+    q.lo = p - a.W + 1;
+    q.lo = q.lo < 0 ? 0 : q.lo > q.L ? q.L : q.lo;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  for (int c = 0; c < C; ++c) {
-    const int64_t at = (r * a.H + h) * D + lane * C + c;
-    if (a.o_f32) static_cast<float*>(a.O)[at] = o[c] * inv;
-    else static_cast<__nv_bfloat16*>(a.O)[at] = __float2bfloat16(o[c] * inv);
+  q.tile0 = q.lo / kTile;
+  q.tiles = (int)ceil_div(q.S - q.tile0 * kTile, kTile);
+  if (q.tiles < 1) q.tiles = 1;
+  q.sets = (int)ceil_div((int64_t)q.n * a.G, kItemRows);
+  return q;
+}
+
+// One segment of a share: part of one item.
+struct Segment {
+  int valid;
+  int r0, n;          // the sequence's first row and nodes
+  int row0, rows;     // the item's first (node, head) row and its rows
+  int hk;
+  int t0, t1;         // its key tiles, counted from tile 0 of the sequence
+  int64_t L, lo;
+  uint64_t any;       // drafted rows that some node sees
+  int slot;           // partial result slot, or -1: the whole item, final
+};
+
+template <int D>
+struct TreeSmem {
+  static constexpr int kHalf = kTile * 128;               // one 64-channel half of a tile
+  static constexpr int kTileBytes = (D / 64) * kHalf;     // 128 rows x D bf16
+  static constexpr int kStages = D == 128 ? 5 : 10;       // K and V tiles in flight, 160 KB
+  static constexpr size_t off_q = 0;                      // 2 row tiles (the second: statistics of merging streams)
+  static constexpr size_t off_kv = 2 * kTileBytes;
+  static constexpr size_t off_bar = off_kv + (size_t)kStages * kTileBytes;
+  static constexpr size_t off_seg = off_bar + 48 * 8;
+  static constexpr size_t off_misc = off_seg + 2 * 128;
+  static constexpr size_t bytes = off_misc + 64 + 1024;
+};
+static_assert(sizeof(Segment) <= 128, "segment slot");
+
+// Position of K / V of key tile t of a segment of n tiles in its stream of loads:
+// the order in which the MMA warp uses them.  Both streams on every tile:
+// K0 V0 K1 V1 ..; alternate tiles: K0 K1 V0 K2 V1 .. (S runs one tile ahead).
+__device__ __forceinline__ int k_place(bool dual, int t) { return dual ? 2 * t : (t == 0 ? 0 : 2 * t - 1); }
+__device__ __forceinline__ int v_place(bool dual, int t, int n) {
+  return dual ? 2 * t + 1 : (t == n - 1 ? 2 * n - 1 : 2 * t + 2);
+}
+
+// Bits [lo, hi) of a 32-bit word (lo and hi anything).
+__device__ __forceinline__ uint32_t bit_range(int64_t lo, int64_t hi) {
+  if (lo < 0) lo = 0;
+  if (hi > 32) hi = 32;
+  if (lo >= hi) return 0u;
+  return (0xFFFFFFFFu >> (32 - (int)(hi - lo))) << (int)lo;
+}
+
+// Visible columns off .. off+31 of a row: committed rows [lo, L), drafted rows by mask.
+__device__ __forceinline__ uint32_t visible(int64_t off, int64_t lo, int64_t L, uint64_t mask) {
+  uint32_t w = bit_range(lo - off, L - off);
+  const int64_t sh = off - L;
+  if (sh >= 0) {
+    if (sh < 64) w |= (uint32_t)(mask >> sh);
+  } else if (sh > -32) {
+    w |= (uint32_t)(mask << -sh);
   }
-  if (a.lse && lane == 0) a.lse[r * a.H + h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  return w;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_attn_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ TreeMaps maps) {
+  using L = TreeSmem<D>;
+  constexpr int kStages = L::kStages;
+  constexpr int HALVES = D / 64;
+  constexpr uint32_t kHalfBytes = L::kHalf;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_q = smem + L::off_q;
+  uint8_t* s_kv = smem + L::off_kv;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::off_bar);
+  uint64_t* kv_full = bar;                  // [kStages] tile landed
+  uint64_t* kv_empty = bar + kStages;       // [kStages] its products complete
+  uint64_t* q_full = bar + 2 * kStages;     // [2] row tile in shared memory
+  uint64_t* q_free = bar + 2 * kStages + 2;   // a segment's QK products complete
+  uint64_t* s_full = bar + 2 * kStages + 3;   // [2] S of a stream's tile complete
+  uint64_t* p_full = bar + 2 * kStages + 5;   // [2] P written
+  uint64_t* o_full = bar + 2 * kStages + 7;   // [2] a stream's last PV of a segment complete
+  uint64_t* o_free = bar + 2 * kStages + 9;   // the segment's outputs read out of TMEM
+  uint64_t* seg_full = bar + 2 * kStages + 10;  // [2] a segment's description is in its slot
+  uint64_t* seg_free = bar + 2 * kStages + 12;  // [2] every role is done with the slot
+  uint64_t* mma_fin = bar + 2 * kStages + 14;
+  uint64_t* ex_full = bar + 2 * kStages + 15;   // statistics of merging streams: written, then read
+  uint8_t* s_seg = smem + L::off_seg;
+  int* misc = reinterpret_cast<int*>(smem + L::off_misc);  // [0] tmem
+  volatile int* s_abort = misc + 1;  // set by the first wait that timed out; every role then stops
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // ---- setup: barriers, TMEM
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 4);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_free[i], kSoftmaxWarps + 1);
+    }
+    mbar_init(q_free, 1);
+    mbar_init(o_free, kSoftmaxWarps);
+    mbar_init(mma_fin, 1);
+    mbar_init(ex_full, kSoftmaxWarps);
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(reinterpret_cast<uint32_t*>(&misc[0]), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = (uint32_t)misc[0];
+  // TMEM columns: the streams' S (and P over it), then their outputs
+  constexpr uint32_t kTmemS = 0, kTmemO = 256;
+
+  // Bounded wait that also stops once any role of this CTA has given up.
+  auto wait = [&](uint64_t* b_, uint32_t ph) -> bool {
+    if (*s_abort) return false;
+    if (mbar_wait(b_, ph, a.status, CSA_ERR_DEVICE_TIMEOUT)) return true;
+    *s_abort = 1;
+    return false;
+  };
+  // the next segment's description (in place until the role releases it), or null
+  auto next_segment = [&](int n) -> const Segment* {
+    if (!wait(&seg_full[n & 1], (uint32_t)((n >> 1) & 1))) return nullptr;
+    const Segment* s = reinterpret_cast<const Segment*>(s_seg + (n & 1) * 128);
+    return s->valid ? s : nullptr;
+  };
+  auto release_segment = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&seg_free[n & 1]);
+  };
+
+  if (warp >= kSoftmaxWarps) regs_decrease<kOtherRegs>();
+  else regs_increase<kSoftmaxRegs>();
+
+  if (warp == kLoadWarp) {
+    // =========================== the share: its segments and their K / V tiles
+    griddep_launch_dependents();
+    // total key tiles; which sequence the share starts in (every lane a stride of
+    // sequences, then the same in order)
+    const bool skip = *reinterpret_cast<volatile int*>(a.status) == CSA_ERR_DEVICE_TIMEOUT;
+    int64_t total = 0;
+    for (int b = lane; b < a.B; b += 32) total += load_seq(a, b, blockIdx.x == 0).total(a.Hk);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    int64_t ctas = total / kMinShare;
+    ctas = ctas < 1 ? 1 : ctas > gridDim.x ? gridDim.x : ctas;
+    const int64_t c = blockIdx.x;
+    int64_t first = c < ctas ? c * total / ctas : 0, last = c < ctas ? (c + 1) * total / ctas : 0;
+    if (skip) first = last = 0;
+    int4 split = make_int4(0, 0, 0, 0);
+    // find the sequence that holds tile `first`
+    int b = 0;
+    int64_t at = 0;  // tiles before sequence b
+    if (first < last) {
+      for (int base = 0; base < a.B; base += 32) {
+        const int64_t mine = base + lane < a.B ? load_seq(a, base + lane, false).total(a.Hk) : 0;
+        int64_t up = mine;  // inclusive prefix
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, up, o);
+          if (lane >= o) up += y;
+        }
+        const uint32_t over = __ballot_sync(0xffffffffu, at + up > first);
+        if (over) {
+          const int w = __ffs(over) - 1;
+          b = base + w;
+          at += __shfl_sync(0xffffffffu, up - mine, w);
+          break;
+        }
+        at += __shfl_sync(0xffffffffu, up, 31);
+      }
+    }
+    int loads = 0;  // tiles fetched so far (ring position)
+    int n = 0;      // segments published
+    bool live = true;
+    for (int64_t g = first; g < last && live; ++n) {
+      Seq q = load_seq(a, b, false);
+      while (g >= at + q.total(a.Hk) && b + 1 < a.B) {
+        at += q.total(a.Hk);
+        q = load_seq(a, ++b, false);
+      }
+      if (q.tiles == 0) break;
+      const int item = (int)((g - at) / q.tiles);
+      Segment s;
+      s.valid = 1;
+      s.r0 = q.r0;
+      s.n = q.n;
+      s.hk = item / q.sets;
+      s.row0 = item % q.sets * kItemRows;
+      const int left = q.n * a.G - s.row0;
+      s.rows = left < kItemRows ? left : kItemRows;
+      const int64_t i0 = at + (int64_t)item * q.tiles, i1 = i0 + q.tiles;  // the item on the line
+      const int64_t end = i1 < last ? i1 : last;
+      s.t0 = (int)(q.tile0 + (g - i0));
+      s.t1 = (int)(q.tile0 + (end - i0));
+      s.L = q.L;
+      s.lo = q.lo;
+      uint64_t any = 0;
+      for (int i = lane; i < q.n; i += 32) any |= a.mask[q.r0 + i];
+      s.any = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32 |
+              __reduce_or_sync(0xffffffffu, (uint32_t)any);
+      if (q.n < 64) s.any &= (1ull << q.n) - 1;
+      const bool whole = g == i0 && end == i1;
+      s.slot = whole ? -1 : (int)(2 * c) + (g == first ? 0 : 1);
+      if (g == i0 && end < i1) {  // the item goes on in the next CTAs: tell the combine
+        int64_t cl = (i1 - 1) * ctas / total;
+        while ((cl + 1) * total / ctas < i1) ++cl;
+        split = make_int4(s.rows, s.slot, (int)(cl - c + 1), 0);
+        // first output row: (r0 * H + hk * G) and the item's rows from row0
+        if (lane == 0) {
+          a.split[2 * c + 1] = make_int4(s.r0, s.hk, s.row0, 0);
+        }
+      }
+      // publish
+      if (n >= 2 && !wait(&seg_free[n & 1], (uint32_t)((n / 2 - 1) & 1))) break;
+      if (lane == 0) {
+        *reinterpret_cast<Segment*>(s_seg + (n & 1) * 128) = s;
+        mbar_arrive(&seg_full[n & 1]);
+      }
+      // K and V tiles
+      const bool dual = s.rows > kTile;
+      const int nt = s.t1 - s.t0;
+      const int box_rows = a.page_shift < 7 ? 1 << a.page_shift : kTile;
+      const int boxes = kTile / box_rows * HALVES;  // per tile, at most 16
+      const int my_row = lane / HALVES * box_rows, my_half = lane % HALVES;
+      for (int i = 0; i < 2 * nt && live; ++i) {
+        // load i of the segment: which tile of which kind
+        int t, kind;
+        if (dual) {
+          t = i >> 1, kind = i & 1;
+        } else if (i == 0 || i == 2 * nt - 1) {
+          t = i == 0 ? 0 : nt - 1, kind = i == 0 ? 0 : 1;
+        } else {
+          kind = (i & 1) ? 0 : 1;
+          t = kind ? i / 2 - 1 : (i + 1) / 2;
+        }
+        const int st = loads % kStages;
+        if (loads >= kStages && !wait(&kv_empty[st], (uint32_t)((loads / kStages - 1) & 1))) {
+          live = false;
+          break;
+        }
+        const int64_t key = (int64_t)(s.t0 + t) * kTile + my_row;
+        const bool need = lane < boxes && key + box_rows > q.lo && key < q.S;
+        int page = 0;
+        if (need) {
+          page = a.table[(int64_t)b * a.max_pages + (key >> a.page_shift)];
+          if (page < 0 || page >= a.n_pages) {
+            report(a.status, CSA_ERR_INDEX);
+            page = a.n_pages > 0 ? (int)a.n_pages : 1;  // outside the map: zeros
+          }
+        }
+        const int count = __popc(__ballot_sync(0xffffffffu, need));
+        if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], (uint32_t)(count * box_rows * 128));
+        __syncwarp();
+        if (need) {
+          const int row = (s.hk << a.page_shift) + (int)(key & ((1 << a.page_shift) - 1));
+          tma_load_3d(s_kv + (size_t)st * L::kTileBytes + my_half * kHalfBytes + my_row * 128,
+                      kind ? &maps.v : &maps.k, &kv_full[st], my_half * 64, row, page);
+        }
+        ++loads;
+      }
+      g = end;
+    }
+    if (lane == 0) a.split[2 * c] = split;
+    // no more segments
+    if (live && (n < 2 || wait(&seg_free[n & 1], (uint32_t)((n / 2 - 1) & 1))) && lane == 0) {
+      reinterpret_cast<Segment*>(s_seg + (n & 1) * 128)->valid = 0;
+      mbar_arrive(&seg_full[n & 1]);
+    }
+    // after an abort, wait (bounded) for the loads still landing in shared memory
+    if (*s_abort && lane == 0)
+      for (int i = loads > kStages ? loads - kStages : 0; i < loads; ++i)
+        mbar_wait(&kv_full[i % kStages], (uint32_t)((i / kStages) & 1));
+  } else if (warp == kMmaWarp) {
+    // =========================== MMA issue
+    const uint32_t sq = smem_u32(s_q), skv = smem_u32(s_kv);
+    bool live = true;
+    int loads = 0;   // ring position of the segment's first tile
+    int duals = 0;   // segments so far that loaded a second row tile
+    int jobs0 = 0, jobs1 = 0;  // tiles so far of the two streams: the phases of their P barriers
+    for (int n = 0; live; ++n) {
+      const Segment* sp = next_segment(n);
+      if (sp == nullptr) break;
+      const Segment& s = *sp;
+      const bool dual = s.rows > kTile;
+      const int nt = s.t1 - s.t0;
+      const int jobs = dual ? 2 * nt : nt;  // job x: stream x & 1, key tile dual ? x / 2 : x
+      if (!wait(&q_full[0], (uint32_t)(n & 1)) || (dual && !wait(&q_full[1], (uint32_t)(duals & 1)))) break;
+      if (dual) ++duals;
+      tc_fence_after();
+      auto issue_s = [&](int x) -> bool {
+        const int st = x & 1, t = dual ? x >> 1 : x;
+        const int at = loads + k_place(dual, t);
+        if (!(dual && st) && !wait(&kv_full[at % kStages], (uint32_t)((at / kStages) & 1))) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t sk = skv + (uint32_t)(at % kStages) * L::kTileBytes;
+          const uint32_t qa = sq + (dual && st ? (uint32_t)L::kTileBytes : 0u);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (uint32_t)((kk >> 2) * kHalfBytes + (kk & 3) * 32);
+            mma_bf16_ss(tbase + kTmemS + st * 128, make_sdesc(qa + off, 16, 1024, kSwizzle128),
+                        make_sdesc(sk + off, 16, 1024, kSwizzle128), idesc_bf16(128, kTile, 0, 0), kk > 0);
+          }
+          mma_commit(&s_full[st]);
+          if (!dual || st) mma_commit(&kv_empty[at % kStages]);
+          if (x == jobs - 1) mma_commit(q_free);
+        }
+        __syncwarp();
+        return true;
+      };
+      live = issue_s(0) && (jobs < 2 || issue_s(1));
+      // the outputs of the segment before must be out of TMEM before the first PV
+      if (live && n > 0) live = wait(o_free, (uint32_t)((n - 1) & 1));
+      tc_fence_after();
+      for (int x = 0; x < jobs && live; ++x) {
+        const int st = x & 1, t = dual ? x >> 1 : x;
+        const int at = loads + v_place(dual, t, nt);
+        if (!wait(&p_full[st], (uint32_t)((st ? jobs1++ : jobs0++) & 1))) {
+          live = false;
+          break;
+        }
+        const uint32_t sv = skv + (uint32_t)(at % kStages) * L::kTileBytes;
+        if (!(dual && st)) {
+          if (!wait(&kv_full[at % kStages], (uint32_t)((at / kStages) & 1))) {
+            live = false;
+            break;
+          }
+          // rows that no node sees hold anything (or were not fetched): zero them
+          const int64_t k0 = (int64_t)(s.t0 + t) * kTile;
+          if (k0 < s.lo || k0 + kTile > s.L) {
+            for (int r = lane >> 3; r < kTile; r += 4) {
+              const int64_t key = k0 + r, draft = key - s.L;
+              if (draft < 0 ? key >= s.lo : draft < 64 && (s.any >> draft & 1)) continue;
+#pragma unroll
+              for (int h = 0; h < HALVES; ++h)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(sv + h * kHalfBytes + r * 128 +
+                                                                              (lane & 7) * 16),
+                             "r"(0)
+                             : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t pcol = tbase + kTmemS + st * 128, o = tbase + kTmemO + st * D;
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            mma_bf16_ts(o, pcol + 8 * ks, make_sdesc(sv + ks * 2048, kHalfBytes, 1024, kSwizzle128),
+                        idesc_bf16(128, D, 0, 1), (x >= 2 || ks > 0) ? 1u : 0u);
+          if (!dual || st) mma_commit(&kv_empty[at % kStages]);
+          if (x + 2 >= jobs) mma_commit(&o_full[st]);
+        }
+        __syncwarp();
+        if (x + 2 < jobs && !issue_s(x + 2)) live = false;
+      }
+      if (jobs == 1) {  // the second stream had nothing: its barrier keeps step
+        if (elect_one()) mma_commit(&o_full[1]);
+        __syncwarp();
+      }
+      loads += 2 * nt;
+      release_segment(n);
+    }
+    // every MMA this warp issued has completed before TMEM is freed
+    if (elect_one()) mma_commit(mma_fin);
+    __syncwarp();
+    mbar_wait(mma_fin, 0);
+  } else if (warp < kSoftmaxWarps) {
+    // =========================== softmax streams (warps 0..3, 4..7): one row per thread
+    const int st = warp >> 2;
+    const int trow = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
+    const uint32_t lane_base = tbase + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t scol = lane_base + kTmemS + st * 128;
+    const float c = a.scale_log2;  // > 0: max of raw logits * c = max of scaled logits
+    int jobs_seen = 0;             // tiles of this stream so far: the phase of its S barrier
+    for (int n = 0;; ++n) {
+      const Segment* sp = next_segment(n);
+      if (sp == nullptr) break;
+      const Segment& s = *sp;
+      const bool dual = s.rows > kTile;
+      const int jobs = dual ? 2 * (s.t1 - s.t0) : s.t1 - s.t0;
+      const int row = trow + (dual && st ? kTile : 0);  // row of the item
+      const bool mine = row < s.rows;
+      const int node = mine ? (s.row0 + row) / a.G : 0;
+      const int64_t orow = (int64_t)(s.r0 + node) * a.H + s.hk * a.G + (mine ? (s.row0 + row) % a.G : 0);
+      uint64_t mask = 0;
+      int64_t lo = 0;
+      if (mine) {
+        mask = a.mask[s.r0 + node] & (s.n < 64 ? (1ull << s.n) - 1 : ~0ull);
+        if (a.W >= 0) {
+          lo = a.pos[s.r0 + node] - a.W + 1;
+          lo = lo < 0 ? 0 : lo > s.L ? s.L : lo;
+        }
+      }
+      // this thread's query row into the stream's row tile (128-byte swizzle)
+      if (n > 0 && !wait(q_free, (uint32_t)((n - 1) & 1))) break;
+      if (st == 0 || dual) {
+        const uint32_t dst = smem_u32(s_q) + (uint32_t)(st * L::kTileBytes + trow * 128);
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) {
+          uint4 v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            v[j] = mine ? *reinterpret_cast<const uint4*>(a.q + orow * D + h * 64 + j * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + h * kHalfBytes +
+                                                                          (uint32_t)((j ^ (trow & 7)) << 4)),
+                         "r"(v[j].x), "r"(v[j].y), "r"(v[j].z), "r"(v[j].w)
+                         : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[st]);
+      }
+      const bool warp_mine = __any_sync(0xffffffffu, mine);
+      float m_run = -INFINITY;
+      float2 l2 = make_float2(0.f, 0.f);
+      bool live = true;
+      for (int x = st; x < jobs; x += 2) {
+        const int64_t base = (int64_t)(s.t0 + (dual ? x >> 1 : x)) * kTile;
+        if (!wait(&s_full[st], (uint32_t)(jobs_seen++ & 1))) {
+          live = false;
+          break;
+        }
+        tc_fence_after();
+        if (warp_mine) {
+          uint32_t v[kTile];
+#pragma unroll
+          for (int j = 0; j < kTile; j += 32) tmem_ld32p(scol + j, v + j);
+          tmem_wait_ld_regs32(v);
+#pragma unroll
+          for (int j = 32; j < kTile; j += 32) tmem_tie32(v + j);
+          // columns out of sight become -inf
+          if (__any_sync(0xffffffffu, !(lo <= base && base + kTile <= s.L))) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t bits = visible(base + 32 * w, lo, s.L, mask);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(bits >> e & 1)) v[32 * w + e] = 0xFF800000u;
+            }
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < kTile; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+          const bool raise = mt > m_run + kRescaleSlack || (m_run == -INFINITY && mt > -INFINITY);
+          const float m_new = raise ? mt : m_run;
+          const float m_use = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: every weight is 0
+          if (__any_sync(0xffffffffu, raise && x >= 2)) {
+            // S of this tile is complete, so the PV of the tile before is, too
+            const float alpha = raise ? fast_exp2(m_run - m_new) : 1.f;
+            l2.x *= alpha, l2.y *= alpha;
+#pragma unroll 1
+            for (int j = 0; j < D; j += 32) {
+              uint32_t o[32];
+              tmem_ld32p(lane_base + kTmemO + st * D + j, o);
+              tmem_wait_ld_regs32(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32p(lane_base + kTmemO + st * D + j, o);
+            }
+          }
+          m_run = m_new;
+          // p = 2^(s c - m); the sums take the unrounded weights, the product with V
+          // their bf16 rounding (the tensor pipe's operand type)
+#pragma unroll
+          for (int j = 0; j < kTile; j += 64) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) {
+              const float p0 = fast_exp2(fmaf(__uint_as_float(v[j + e]), c, -m_use));
+              const float p1 = fast_exp2(fmaf(__uint_as_float(v[j + e + 1]), c, -m_use));
+              l2.x += p0, l2.y += p1;
+              pk[e / 2] = pack_bf16x2(p0, p1);
+            }
+            tmem_st32p(scol + j / 2, pk);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[st]);
+      }
+      // ---- outputs
+      if (!live || !wait(&o_full[st], (uint32_t)(n & 1))) break;
+      float l = l2.x + l2.y;
+      float f[2] = {st == 0 ? 1.f : 0.f, st == 0 ? 0.f : 1.f};  // weights of the two accumulators
+      if (!dual) {
+        // the streams hold the same rows: exchange (max, sum), then each writes half the channels
+        if (!wait(&o_full[st ^ 1], (uint32_t)(n & 1))) break;
+        float2* ex = reinterpret_cast<float2*>(s_q + L::kTileBytes);
+        ex[st * kTile + trow] = make_float2(m_run, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ex_full);
+        if (!wait(ex_full, 0)) break;
+        const float2 e0 = ex[trow], e1 = ex[kTile + trow];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ex_full);
+        if (!wait(ex_full, 1)) break;
+        m_run = fmaxf(e0.x, e1.x);
+        f[0] = e0.y > 0.f ? fast_exp2(e0.x - m_run) : 0.f;
+        f[1] = e1.y > 0.f ? fast_exp2(e1.x - m_run) : 0.f;
+        l = e0.y * f[0] + e1.y * f[1];
+      }
+      tc_fence_after();
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      f[0] *= inv, f[1] *= inv;
+      const float lse2 = l > 0.f ? m_run + log2f(l) : -INFINITY;
+      const int64_t prow = (int64_t)s.slot * a.part_rows + row;
+      const bool part = s.slot >= 0, f32 = part || a.o_f32;
+      float* of = part ? a.part_o + prow * D : static_cast<float*>(a.O) + orow * D;
+      __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.O) + orow * D;
+      const int c0 = !dual && st ? D / 2 : 0, c1 = !dual && !st ? D / 2 : D;
+      if (warp_mine) {
+#pragma unroll 1
+        for (int j = c0; j < c1; j += 32) {
+          uint32_t x0[32], x1[32];
+          float o[32];
+          const bool both = !dual;
+          tmem_ld32p(lane_base + kTmemO + (both ? 0 : st * D) + j, x0);
+          if (both) tmem_ld32p(lane_base + kTmemO + D + j, x1);
+          tmem_wait_ld_regs32(x0);
+          if (both) tmem_tie32(x1);
+          const float w0 = both ? f[0] : f[st], w1 = both ? f[1] : 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            // an accumulator without a key holds no data: weight 0 exactly
+            o[e] = w0 != 0.f ? __uint_as_float(x0[e]) * w0 : 0.f;
+            if (w1 != 0.f) o[e] = fmaf(__uint_as_float(x1[e]), w1, o[e]);
+          }
+          if (mine) {
+            if (f32) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4*>(of + j + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+                *reinterpret_cast<uint4*>(ob + j + e) =
+                    make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
+                               pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+            }
+          }
+        }
+      }
+      if (mine && (dual || st == 0)) {
+        if (part) a.part_lse[prow] = lse2;
+        else if (a.lse) a.lse[orow] = lse2 * kLn2;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
+      release_segment(n);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// Items that several CTAs share: CTA c of the attention started one and recorded
+//   split[2c] = (rows, slot of its own part, parts, -), split[2c+1] = (first row of
+//   the sequence, key head, first row of the item); parts 2, 3, .. are the first
+//   slots of CTAs c+1, c+2, ..
+// O = sum_i 2^(lse_i - lse) O_i with lse = log2 sum_i 2^lse_i, in the parts' order.
+// A warp takes a row; when there are fewer rows than blocks, the eight warps of a
+// block share the parts of one row.
+constexpr int kMaxCtas = 1024;
+
+template <int D>
+__global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ TreeArgs a, int ctas) {
+  __shared__ int s_rows[kMaxCtas + 1];  // rows before CTA c's item
+  __shared__ float s_o[8][D];
+  __shared__ float s_l[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_wait();  // the partial results come from the attention kernel before
+  if (warp == 0) {
+    int sum = 0;
+    for (int base = 0; base < ctas; base += 32) {
+      const int4 e = base + lane < ctas ? a.split[2 * (base + lane)] : make_int4(0, 0, 0, 0);
+      const int mine = e.z > 0 ? e.x : 0;
+      int up = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o) up += y;
+      }
+      if (base + lane < ctas) s_rows[base + lane] = sum + up - mine;
+      sum += __shfl_sync(0xffffffffu, up, 31);
+    }
+    if (lane == 0) s_rows[ctas] = sum;
+  }
+  __syncthreads();
+  const int rows = s_rows[ctas];
+  const bool shared = rows <= (int)gridDim.x;  // a block per row
+  const int step = shared ? gridDim.x : gridDim.x * 8;
+  for (int i = shared ? blockIdx.x : blockIdx.x * 8 + warp; i < rows; i += step) {
+    int c0 = 0, c1 = ctas;  // the last c with s_rows[c] <= i has rows
+    while (c1 - c0 > 1) {
+      const int mid = (c0 + c1) / 2;
+      if (s_rows[mid] <= i) c0 = mid;
+      else c1 = mid;
+    }
+    const int4 e = a.split[2 * c0], w = a.split[2 * c0 + 1];
+    const int row = i - s_rows[c0];
+    const int parts = e.z;
+    auto slot = [&](int p) { return p == 0 ? e.y : 2 * (c0 + p); };
+    // the largest lse of all parts, then the weighted sums of this warp's
+    float m = -INFINITY;
+    for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.part_lse[(int64_t)slot(p) * a.part_rows + row]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    constexpr int C = D / 32;
+    float acc[C] = {};
+    float l = 0.f;
+    if (m > -INFINITY) {
+#pragma unroll 8
+      for (int p = shared ? warp : 0; p < parts; p += shared ? 8 : 1) {
+        const int64_t at = (int64_t)slot(p) * a.part_rows + row;
+        const float wt = exp2f(a.part_lse[at] - m);
+        l += wt;
+#pragma unroll
+        for (int j = 0; j < C; ++j) acc[j] = fmaf(wt, a.part_o[at * D + 32 * j + lane], acc[j]);
+      }
+    }
+    if (shared) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) s_o[warp][32 * j + lane] = acc[j];
+      if (lane == 0) s_l[warp] = l;
+      __syncthreads();
+      if (warp == 0) {
+        for (int p = 1; p < 8; ++p) {
+          l += s_l[p];
+#pragma unroll
+          for (int j = 0; j < C; ++j) acc[j] += s_o[p][32 * j + lane];
+        }
+      }
+      __syncthreads();
+      if (warp != 0) continue;
+    }
+    const int nh = w.z + row;  // (node, head) of the sequence's rows for this key head
+    const int64_t orow = (int64_t)(w.x + nh / a.G) * a.H + w.y * a.G + nh % a.G;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int64_t at = orow * D + 32 * j + lane;
+      if (a.o_f32) static_cast<float*>(a.O)[at] = acc[j] * inv;
+      else static_cast<__nv_bfloat16*>(a.O)[at] = __float2bfloat16(acc[j] * inv);
+    }
+    if (a.lse && lane == 0) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  }
+}
+
+// K / V pages as [n_pages][Hk * page][d] bf16, fetched in boxes of up to 128 rows of
+// one page x 64 channels (128-byte swizzle).
+bool page_map(CUtensorMap* m, const void* base, int64_t n_pages, int Hk, int page, int d) {
+  EncodeFn enc = get_encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)Hk * page, (cuuint64_t)n_pages};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)Hk * page * d * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)(page < kTile ? page : kTile), 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTAs of a call: one per SM, fewer when even the longest sequences that the
+// tables can hold give less than kMinShare key tiles each.
+int tree_ctas(int B, int64_t R, int H, int Hk, int page, int max_pages) {
+  const int64_t sms = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
+  const int64_t nodes = R < kMaxNodes ? R : kMaxNodes;
+  const int64_t seqs = B < R ? B : R;  // with a node
+  const int64_t items = Hk * (seqs + R * (H / Hk) / kItemRows);
+  const int64_t tiles = ceil_div((int64_t)max_pages * page, kTile) + (nodes > 0 ? 1 : 0);
+  const int64_t most = items * tiles / kMinShare;
+  return (int)(most < 1 ? 1 : most < sms ? most : sms);
+}
+
+int part_rows(int64_t R, int H, int Hk) {
+  const int64_t rows = (R < kMaxNodes ? R : kMaxNodes) * (H / Hk);
+  return (int)(rows < kItemRows ? rows : kItemRows);
+}
+
+template <int D>
+cudaError_t launch_tree(const TreeArgs& a, const TreeMaps& maps, int ctas, cudaStream_t stream) {
+  constexpr size_t smem = TreeSmem<D>::bytes;
+  static_assert(smem <= 227 * 1024, "shared memory of one CTA");
+  cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess)
+    e = launch_kernel(tree_attn_kernel<D>, dim3(ctas), dim3(kThreads), smem, stream, false, a, maps);
+  if (e == cudaSuccess && ctas > 1)
+    e = launch_kernel(tree_combine_kernel<D>, dim3(4 * sm_count()), dim3(256), 0, stream, true, a, ctas);
+  return e;
 }
 
 }  // namespace
@@ -93,7 +858,13 @@ using namespace csa;
 
 extern "C" {
 
-size_t csa_tree_attn_workspace_bytes(int, int64_t, int, int, int, int, int) { return kWorkspaceHeader; }
+// [header][split 2 x int4 per CTA][partial lse][partial O], two slots per CTA
+size_t csa_tree_attn_workspace_bytes(int B, int64_t R, int H, int Hk, int d, int page, int max_pages) {
+  if (B <= 0 || R <= 0 || H <= 0 || Hk <= 0 || H < Hk || page <= 0 || max_pages <= 0) return kWorkspaceHeader;
+  const int ctas = tree_ctas(B, R, H, Hk, page, max_pages);
+  const size_t rows = ctas > 1 ? (size_t)2 * ctas * part_rows(R, H, Hk) : 0;
+  return kWorkspaceHeader + align256((size_t)ctas * 32) + align256(rows * 4) + align256(rows * d * 4);
+}
 
 int csa_tree_attn(const void* q, const void* Kpages, const void* Vpages, const int32_t* block_table,
                   const int32_t* seq_lens, const int32_t* q_start, const uint64_t* mask, const int64_t* pos, int64_t R,
@@ -103,7 +874,7 @@ int csa_tree_attn(const void* q, const void* Kpages, const void* Vpages, const i
       !(std::isfinite(scale) && scale > 0.f) || !valid_odtype(o_dtype))
     return CSA_ERR_INVALID_ARG;
   if ((d != 64 && d != 128) || !valid_page(page) || H > 1024 || H % Hk != 0) return CSA_ERR_UNSUPPORTED_SHAPE;
-  if ((int64_t)max_pages * page > 0x7FFFFFFF) return CSA_ERR_UNSUPPORTED_SHAPE;
+  if ((int64_t)max_pages * page > 0x7FFFFFFF - kTile || n_pages > 0x7FFFFFFE) return CSA_ERR_UNSUPPORTED_SHAPE;
   int rc = check_ws(workspace, workspace_bytes, csa_tree_attn_workspace_bytes(B, R, H, Hk, d, page, max_pages));
   if (rc) return rc;
   if (R == 0 || B == 0) return CSA_OK;
@@ -114,8 +885,6 @@ int csa_tree_attn(const void* q, const void* Kpages, const void* Vpages, const i
   if ((rc = check_opt(lse))) return rc;
   TreeArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(q);
-  a.Kp = static_cast<const __nv_bfloat16*>(Kpages);
-  a.Vp = static_cast<const __nv_bfloat16*>(Vpages);
   a.table = block_table;
   a.lens = seq_lens;
   a.q_start = q_start;
@@ -126,6 +895,7 @@ int csa_tree_attn(const void* q, const void* Kpages, const void* Vpages, const i
   a.B = B;
   a.H = H;
   a.Hk = Hk;
+  a.G = H / Hk;
   a.max_pages = max_pages;
   while ((1 << a.page_shift) < page) ++a.page_shift;
   a.W = W;
@@ -134,10 +904,21 @@ int csa_tree_attn(const void* q, const void* Kpages, const void* Vpages, const i
   a.o_f32 = o_dtype == CSA_F32;
   a.lse = lse;
   a.status = status_word(workspace);
-  const int64_t grid = ceil_div(R * H, 4);
-  if (grid > 0x7FFFFFFF) return CSA_ERR_UNSUPPORTED_SHAPE;
-  cudaError_t e = launch_kernel(d == 128 ? tree_attn_kernel<128> : tree_attn_kernel<64>, dim3((unsigned)grid), dim3(128),
-                                0, (cudaStream_t)stream, false, a);
+  const int ctas = tree_ctas(B, R, H, Hk, page, max_pages);
+  a.part_rows = part_rows(R, H, Hk);
+  uint8_t* w = static_cast<uint8_t*>(workspace) + kWorkspaceHeader;
+  a.split = reinterpret_cast<int4*>(w);
+  w += align256((size_t)ctas * 32);
+  a.part_lse = reinterpret_cast<float*>(w);
+  a.part_o = reinterpret_cast<float*>(w + align256((size_t)2 * ctas * a.part_rows * 4));
+  TreeMaps maps;
+  const void* kb = n_pages > 0 ? Kpages : q;  // no pages: every page number is out of bounds, nothing is fetched
+  const void* vb = n_pages > 0 ? Vpages : q;
+  if (!page_map(&maps.k, kb, n_pages > 0 ? n_pages : 1, n_pages > 0 ? Hk : 1, page, d) ||
+      !page_map(&maps.v, vb, n_pages > 0 ? n_pages : 1, n_pages > 0 ? Hk : 1, page, d))
+    return cuda_fail(cudaErrorInvalidValue);
+  cudaError_t e = d == 128 ? launch_tree<128>(a, maps, ctas, (cudaStream_t)stream)
+                           : launch_tree<64>(a, maps, ctas, (cudaStream_t)stream);
   return e == cudaSuccess ? CSA_OK : cuda_fail(e);
 }
 
