@@ -278,10 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(&seg_free[n & 1]);
   };
 
-  if (warp >= kSoftmaxWarps) regs_decrease<kOtherRegs>();
-  else regs_increase<kSoftmaxRegs>();
-
   if (warp == kLoadWarp) {
+    regs_decrease<kOtherRegs>();
     // =========================== the share: its segments and their K / V tiles
     griddep_launch_dependents();
     // total key tiles; which sequence the share starts in (every lane a stride of
@@ -421,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = loads > kStages ? loads - kStages : 0; i < loads; ++i)
         mbar_wait(&kv_full[i % kStages], (uint32_t)((i / kStages) & 1));
   } else if (warp == kMmaWarp) {
+    regs_decrease<kOtherRegs>();
     // =========================== MMA issue
     const uint32_t sq = smem_u32(s_q), skv = smem_u32(s_kv);
     bool live = true;
@@ -516,7 +515,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) mma_commit(mma_fin);
     __syncwarp();
     mbar_wait(mma_fin, 0);
-  } else if (warp < kSoftmaxWarps) {
+  } else if (warp > kMmaWarp) {
+    regs_decrease<kOtherRegs>();
+  } else {
+    regs_increase<kSoftmaxRegs>();
     // =========================== softmax streams (warps 0..3, 4..7): one row per thread
     const int st = warp >> 2;
     const int trow = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
