@@ -110,11 +110,12 @@ def _out(O, like, shape, out_dtype, name="O"):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # (with the device's number torch skips looking it up, several microseconds a call)
+    return torch.cuda.current_stream(torch.cuda.current_device()).cuda_stream
 
 
 def _dev(t, dtype, name, ndim=None):

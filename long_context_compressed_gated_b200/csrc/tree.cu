@@ -9,9 +9,9 @@
 // Work.  The rows of one (sequence, key head) are its nodes times the G = H/Hk
 // query heads that share the key head, 128 to a tensor tile (TMEM lane = row).
 // Up to 256 rows make one item, which walks the keys of its sequence in tiles of
-// 128 from the first one that any row sees.  All items' key tiles form one line,
-// cut into equal shares, one per CTA (one CTA per SM, persistent): lengths may be
-// as ragged as they like.  A share that covers an item only in part writes an
+// 128 from the first one that any row sees.  All items' key tiles, those of an item
+// of two row tiles counted twice, form one line, cut into equal shares, one per CTA
+// (one CTA per SM, persistent): lengths may be as ragged as they like.  A share that covers an item only in part writes an
 // fp32 partial (O, lse); tree_combine_kernel merges those.  Lengths are read on
 // the device, so the cut follows them in a captured graph.
 //
@@ -65,7 +65,7 @@ constexpr int kThreads = 384;       // three warpgroups (the last two warps idle
 // row of S, take 208 and the third group keeps 88 (2 * 208 + 88 = 3 * 168).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kMaxNodes = 64;       // bits of a mask
-constexpr int kMinShare = 8;        // key tiles a CTA takes at least
+constexpr int kMinShare = 8;        // positions of that line a CTA takes at least
 constexpr float kRescaleSlack = 8.0f;  // raise the running max only when it grows by > 2^8
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -99,8 +99,8 @@ struct Seq {
   int64_t lo;       // first row that any node may see
   int64_t tile0;    // first key tile
   int tiles;        // key tiles (one at least: an item without keys still writes its rows)
-  int sets;         // items per key head: ceil(n * G / 256)
-  __device__ int64_t total(int Hk) const { return (int64_t)tiles * sets * Hk; }
+  int units;        // row tiles per key head: ceil(n * G / 128)
+  __device__ int64_t total(int Hk) const { return (int64_t)tiles * units * Hk; }
 };
 
 // 2^x with the SFU (ex2.approx, ~2 ulp; -inf -> +0).
@@ -123,7 +123,7 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b, bool tell) {
     q.n = 0;
   }
   if (q.n == 0) {
-    q.tiles = q.sets = 0;
+    q.tiles = q.units = 0;
     q.tile0 = 0;
     return q;
   }
@@ -140,7 +140,7 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b, bool tell) {
   q.tile0 = q.lo / kTile;
   q.tiles = (int)ceil_div(q.S - q.tile0 * kTile, kTile);
   if (q.tiles < 1) q.tiles = 1;
-  q.sets = (int)ceil_div((int64_t)q.n * a.G, kItemRows);
+  q.units = (int)ceil_div((int64_t)q.n * a.G, kTile);
   return q;
 }
 
@@ -178,6 +178,19 @@ __device__ __forceinline__ int v_place(bool dual, int t, int n) {
   return dual ? 2 * t + 1 : (t == n - 1 ? 2 * n - 1 : 2 * t + 2);
 }
 
+__device__ __forceinline__ void st_shared4(uint32_t addr, const float* v) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
+               : "memory");
+}
+__device__ __forceinline__ float4 ld_shared4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // Bits [lo, hi) of a 32-bit word (lo and hi anything).
 __device__ __forceinline__ uint32_t bit_range(int64_t lo, int64_t hi) {
   if (lo < 0) lo = 0;
@@ -213,15 +226,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* kv_full = bar;                  // [kStages] tile landed
   uint64_t* kv_empty = bar + kStages;       // [kStages] its products complete
   uint64_t* q_full = bar + 2 * kStages;     // [2] row tile in shared memory
-  uint64_t* q_free = bar + 2 * kStages + 2;   // a segment's QK products complete
-  uint64_t* s_full = bar + 2 * kStages + 3;   // [2] S of a stream's tile complete
-  uint64_t* p_full = bar + 2 * kStages + 5;   // [2] P written
-  uint64_t* o_full = bar + 2 * kStages + 7;   // [2] a stream's last PV of a segment complete
-  uint64_t* o_free = bar + 2 * kStages + 9;   // the segment's outputs read out of TMEM
-  uint64_t* seg_full = bar + 2 * kStages + 10;  // [2] a segment's description is in its slot
-  uint64_t* seg_free = bar + 2 * kStages + 12;  // [2] every role is done with the slot
-  uint64_t* mma_fin = bar + 2 * kStages + 14;
-  uint64_t* ex_full = bar + 2 * kStages + 15;   // statistics of merging streams: written, then read
+  uint64_t* s_full = bar + 2 * kStages + 2;   // [2] S of a stream's tile complete
+  uint64_t* p_full = bar + 2 * kStages + 4;   // [2] P written
+  uint64_t* o_full = bar + 2 * kStages + 6;   // [2] a stream's last PV of a segment complete
+  uint64_t* o_free = bar + 2 * kStages + 8;   // the segment's outputs read out of TMEM
+  uint64_t* seg_full = bar + 2 * kStages + 9;  // [2] a segment's description is in its slot
+  uint64_t* seg_free = bar + 2 * kStages + 11;  // [2] every role is done with the slot
+  uint64_t* mma_fin = bar + 2 * kStages + 13;
+  uint64_t* ex_full = bar + 2 * kStages + 14;   // statistics of merging streams: written, then read
   uint8_t* s_seg = smem + L::off_seg;
   int* misc = reinterpret_cast<int*>(smem + L::off_misc);  // [0] tmem
   volatile int* s_abort = misc + 1;  // set by the first wait that timed out; every role then stops
@@ -242,7 +254,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&seg_full[i], 1);
       mbar_init(&seg_free[i], kSoftmaxWarps + 1);
     }
-    mbar_init(q_free, 1);
     mbar_init(o_free, kSoftmaxWarps);
     mbar_init(mma_fin, 1);
     mbar_init(ex_full, kSoftmaxWarps);
@@ -262,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Bounded wait that also stops once any role of this CTA has given up.
   auto wait = [&](uint64_t* b_, uint32_t ph) -> bool {
+    if (mbar_try_wait(b_, ph)) return true;
     if (*s_abort) return false;
     if (mbar_wait(b_, ph, a.status, CSA_ERR_DEVICE_TIMEOUT)) return true;
     *s_abort = 1;
@@ -320,26 +332,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     int loads = 0;  // tiles fetched so far (ring position)
     int n = 0;      // segments published
     bool live = true;
-    for (int64_t g = first; g < last && live; ++n) {
+    for (int64_t g = first; g < last && live;) {
       Seq q = load_seq(a, b, false);
       while (g >= at + q.total(a.Hk) && b + 1 < a.B) {
         at += q.total(a.Hk);
         q = load_seq(a, ++b, false);
       }
       if (q.tiles == 0) break;
-      const int item = (int)((g - at) / q.tiles);
+      // the item that holds position g: a key head's items of two row tiles, then perhaps
+      // one of a single; every key tile of an item is as long as its row tiles
+      const int64_t head = (int64_t)q.tiles * q.units;  // positions of one key head
       Segment s;
       s.valid = 1;
       s.r0 = q.r0;
       s.n = q.n;
-      s.hk = item / q.sets;
-      s.row0 = item % q.sets * kItemRows;
+      s.hk = (int)((g - at) / head);
+      const int set = (int)((g - at - s.hk * head) / (2 * q.tiles));
+      s.row0 = set * kItemRows;
       const int left = q.n * a.G - s.row0;
       s.rows = left < kItemRows ? left : kItemRows;
-      const int64_t i0 = at + (int64_t)item * q.tiles, i1 = i0 + q.tiles;  // the item on the line
+      const int wide = s.rows > kTile ? 2 : 1;
+      const int64_t i0 = at + s.hk * head + (int64_t)set * 2 * q.tiles, i1 = i0 + (int64_t)wide * q.tiles;
       const int64_t end = i1 < last ? i1 : last;
-      s.t0 = (int)(q.tile0 + (g - i0));
-      s.t1 = (int)(q.tile0 + (end - i0));
+      // a key tile goes to the share that holds its first position
+      const int t0 = (int)ceil_div(g - i0, wide), t1 = (int)ceil_div(end - i0, wide);
+      g = end;
+      if (t0 == t1) continue;
+      s.t0 = (int)q.tile0 + t0;
+      s.t1 = (int)q.tile0 + t1;
       s.L = q.L;
       s.lo = q.lo;
       uint64_t any = 0;
@@ -347,11 +367,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       s.any = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32 |
               __reduce_or_sync(0xffffffffu, (uint32_t)any);
       if (q.n < 64) s.any &= (1ull << q.n) - 1;
-      const bool whole = g == i0 && end == i1;
-      s.slot = whole ? -1 : (int)(2 * c) + (g == first ? 0 : 1);
-      if (g == i0 && end < i1) {  // the item goes on in the next CTAs: tell the combine
-        int64_t cl = (i1 - 1) * ctas / total;
-        while ((cl + 1) * total / ctas < i1) ++cl;
+      s.slot = t0 == 0 && t1 == q.tiles ? -1 : (int)(2 * c) + (n == 0 ? 0 : 1);
+      if (t0 == 0 && t1 < q.tiles) {  // the item goes on in the next CTAs: tell the combine
+        const int64_t tail = i0 + (int64_t)wide * (q.tiles - 1);  // its last tile
+        int64_t cl = tail * ctas / total;
+        while ((cl + 1) * total / ctas <= tail) ++cl;
         split = make_int4(s.rows, s.slot, (int)(cl - c + 1), 0);
         // first output row: (r0 * H + hk * G) and the item's rows from row0
         if (lane == 0) {
@@ -406,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++loads;
       }
-      g = end;
+      ++n;
     }
     if (lane == 0) a.split[2 * c] = split;
     // no more segments
@@ -421,10 +441,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     regs_decrease<kOtherRegs>();
     // =========================== MMA issue
-    const uint32_t sq = smem_u32(s_q), skv = smem_u32(s_kv);
+    // operand descriptors of the first row tile, of a K and of a V tile in stage 0; other
+    // places are added to the address field (16-byte units)
+    const uint32_t skv = smem_u32(s_kv);
+    const uint64_t q_desc = make_sdesc(smem_u32(s_q), 16, 1024, kSwizzle128);
+    const uint64_t k_desc = make_sdesc(skv, 16, 1024, kSwizzle128);
+    const uint64_t v_desc = make_sdesc(skv, kHalfBytes, 1024, kSwizzle128);
+    constexpr uint32_t kTile16 = L::kTileBytes / 16;
     bool live = true;
     int loads = 0;   // ring position of the segment's first tile
     int duals = 0;   // segments so far that loaded a second row tile
+    uint32_t steps = 0xFFu;    // steps of 16 keys of the current V tile that some row sees
     int jobs0 = 0, jobs1 = 0;  // tiles so far of the two streams: the phases of their P barriers
     for (int n = 0; live; ++n) {
       const Segment* sp = next_segment(n);
@@ -442,17 +469,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(dual && st) && !wait(&kv_full[at % kStages], (uint32_t)((at / kStages) & 1))) return false;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t sk = skv + (uint32_t)(at % kStages) * L::kTileBytes;
-          const uint32_t qa = sq + (dual && st ? (uint32_t)L::kTileBytes : 0u);
+          const uint64_t qd = q_desc + (dual && st ? kTile16 : 0u);
+          const uint64_t kd = k_desc + (uint32_t)(at % kStages) * kTile16;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (uint32_t)((kk >> 2) * kHalfBytes + (kk & 3) * 32);
-            mma_bf16_ss(tbase + kTmemS + st * 128, make_sdesc(qa + off, 16, 1024, kSwizzle128),
-                        make_sdesc(sk + off, 16, 1024, kSwizzle128), idesc_bf16(128, kTile, 0, 0), kk > 0);
+            const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16;
+            mma_bf16_ss(tbase + kTmemS + st * 128, qd + off, kd + off, idesc_bf16(128, kTile, 0, 0), kk > 0);
           }
           mma_commit(&s_full[st]);
           if (!dual || st) mma_commit(&kv_empty[at % kStages]);
-          if (x == jobs - 1) mma_commit(q_free);
         }
         __syncwarp();
         return true;
@@ -468,24 +493,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           live = false;
           break;
         }
-        const uint32_t sv = skv + (uint32_t)(at % kStages) * L::kTileBytes;
         if (!(dual && st)) {
           if (!wait(&kv_full[at % kStages], (uint32_t)((at / kStages) & 1))) {
             live = false;
             break;
           }
-          // rows that no node sees hold anything (or were not fetched): zero them
+          // Rows that no node sees hold anything (or were not fetched).  Sixteen keys are one
+          // step of the product: steps without a visible row are left out, the hidden rows of
+          // the others zeroed.
           const int64_t k0 = (int64_t)(s.t0 + t) * kTile;
+          steps = 0xFFu;
           if (k0 < s.lo || k0 + kTile > s.L) {
-            for (int r = lane >> 3; r < kTile; r += 4) {
-              const int64_t key = k0 + r, draft = key - s.L;
-              if (draft < 0 ? key >= s.lo : draft < 64 && (s.any >> draft & 1)) continue;
+            const uint32_t seen = visible(k0 + 16 * (lane & 7), s.lo, s.L, s.any) & 0xFFFFu;
+            steps = __ballot_sync(0xffffffffu, seen != 0) & 0xFFu;
+            if (steps == 0) steps = 1;  // (a segment without any visible row still writes its output)
+            uint32_t mend = __ballot_sync(0xffffffffu, seen != 0xFFFFu) & steps;
+            while (mend != 0) {
+              const int ks = __ffs(mend) - 1;
+              mend &= mend - 1;
+              if (!(__shfl_sync(0xffffffffu, seen, ks) >> (lane >> 1) & 1)) {
+                const uint32_t row = skv + (uint32_t)(at % kStages) * L::kTileBytes +
+                                     (uint32_t)(16 * ks + (lane >> 1)) * 128 + (uint32_t)(lane & 1) * 64;
 #pragma unroll
-              for (int h = 0; h < HALVES; ++h)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(sv + h * kHalfBytes + r * 128 +
-                                                                              (lane & 7) * 16),
-                             "r"(0)
-                             : "memory");
+                for (int i = 0; i < 4 * HALVES; ++i)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + (i >> 2) * kHalfBytes +
+                                                                                (i & 3) * 16),
+                               "r"(0)
+                               : "memory");
+              }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -494,10 +529,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (elect_one()) {
           const uint32_t pcol = tbase + kTmemS + st * 128, o = tbase + kTmemO + st * D;
+          const uint64_t vd = v_desc + (uint32_t)(at % kStages) * kTile16;
 #pragma unroll
           for (int ks = 0; ks < kTile / 16; ++ks)
-            mma_bf16_ts(o, pcol + 8 * ks, make_sdesc(sv + ks * 2048, kHalfBytes, 1024, kSwizzle128),
-                        idesc_bf16(128, D, 0, 1), (x >= 2 || ks > 0) ? 1u : 0u);
+            if (steps >> ks & 1)
+              mma_bf16_ts(o, pcol + 8 * ks, vd + ks * 128, idesc_bf16(128, D, 0, 1),
+                          (x >= 2 || (steps & ((1u << ks) - 1))) ? 1u : 0u);
           if (!dual || st) mma_commit(&kv_empty[at % kStages]);
           if (x + 2 >= jobs) mma_commit(&o_full[st]);
         }
@@ -545,22 +582,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           lo = lo < 0 ? 0 : lo > s.L ? s.L : lo;
         }
       }
-      // this thread's query row into the stream's row tile (128-byte swizzle)
-      if (n > 0 && !wait(q_free, (uint32_t)((n - 1) & 1))) break;
+      // this warp's query rows into the stream's row tile (128-byte swizzle).  The products
+      // that read the rows before are complete: this warp has seen the last PV (o_full) of
+      // every stream that used the tile
       if (st == 0 || dual) {
-        const uint32_t dst = smem_u32(s_q) + (uint32_t)(st * L::kTileBytes + trow * 128);
+        // D/8 lanes copy a row, 16 bytes each
+        constexpr int LPR = D / 8, RPW = 32 / LPR;
+        const int ch = lane % LPR;
+        const uint32_t dst = smem_u32(s_q) + (uint32_t)(st * L::kTileBytes + (ch >> 3) * kHalfBytes);
+        const int64_t off = mine ? orow * D : -1;
 #pragma unroll
-        for (int h = 0; h < HALVES; ++h) {
+        for (int i0 = 0; i0 < 32; i0 += 8 * RPW) {
           uint4 v[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            v[j] = mine ? *reinterpret_cast<const uint4*>(a.q + orow * D + h * 64 + j * 8) : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < 8; ++i) {
+            const int64_t from = __shfl_sync(0xffffffffu, off, i0 + i * RPW + lane / LPR);
+            v[i] = from >= 0 ? *reinterpret_cast<const uint4*>(a.q + from + 8 * ch) : make_uint4(0, 0, 0, 0);
+          }
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + h * kHalfBytes +
-                                                                          (uint32_t)((j ^ (trow & 7)) << 4)),
-                         "r"(v[j].x), "r"(v[j].y), "r"(v[j].z), "r"(v[j].w)
+          for (int i = 0; i < 8; ++i) {
+            const int r = (warp & 3) * 32 + i0 + i * RPW + lane / LPR;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + r * 128 +
+                                                                          (uint32_t)(((ch & 7) ^ (r & 7)) << 4)),
+                         "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
                          : "memory");
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -576,6 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           live = false;
           break;
         }
+        __syncwarp();
         tc_fence_after();
         if (warp_mine) {
           uint32_t v[kTile];
@@ -657,43 +704,67 @@ __global__ void __launch_bounds__(kThreads, 1)
         f[1] = e1.y > 0.f ? fast_exp2(e1.x - m_run) : 0.f;
         l = e0.y * f[0] + e1.y * f[1];
       }
+      __syncwarp();
       tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
       f[0] *= inv, f[1] *= inv;
       const float lse2 = l > 0.f ? m_run + log2f(l) : -INFINITY;
+      // rows of this warp, 32 channels at a time: scaled, staged in the shared memory of the
+      // warp's own query rows (free now, and no other warp writes there; 16-byte pieces
+      // swizzled by row), written out by whole rows
       const int64_t prow = (int64_t)s.slot * a.part_rows + row;
       const bool part = s.slot >= 0, f32 = part || a.o_f32;
-      float* of = part ? a.part_o + prow * D : static_cast<float*>(a.O) + orow * D;
-      __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.O) + orow * D;
+      const int64_t off = mine ? (part ? prow : orow) * D : -1;
+      float* of = part ? a.part_o : static_cast<float*>(a.O);
+      __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.O);
       const int c0 = !dual && st ? D / 2 : 0, c1 = !dual && !st ? D / 2 : D;
+      const bool both = !dual;
+      const float w0 = both || st == 0 ? f[0] : f[1], w1 = both ? f[1] : 0.f;
       if (warp_mine) {
+        const uint32_t stage = smem_u32(s_q) + (uint32_t)(st * L::kTileBytes + (warp & 3) * 32 * 128);
 #pragma unroll 1
         for (int j = c0; j < c1; j += 32) {
-          uint32_t x0[32], x1[32];
+          uint32_t x0[32];
           float o[32];
-          const bool both = !dual;
+          __syncwarp();  // (the pieces staged before have been read)
           tmem_ld32p(lane_base + kTmemO + (both ? 0 : st * D) + j, x0);
-          if (both) tmem_ld32p(lane_base + kTmemO + D + j, x1);
           tmem_wait_ld_regs32(x0);
-          if (both) tmem_tie32(x1);
-          const float w0 = both ? f[0] : f[st], w1 = both ? f[1] : 0.f;
+          // an accumulator without a key holds no data: weight 0 exactly
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            // an accumulator without a key holds no data: weight 0 exactly
-            o[e] = w0 != 0.f ? __uint_as_float(x0[e]) * w0 : 0.f;
-            if (w1 != 0.f) o[e] = fmaf(__uint_as_float(x1[e]), w1, o[e]);
+          for (int e = 0; e < 32; ++e) o[e] = w0 != 0.f ? __uint_as_float(x0[e]) * w0 : 0.f;
+          if (both) {
+            tmem_ld32p(lane_base + kTmemO + D + j, x0);
+            tmem_wait_ld_regs32(x0);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (w1 != 0.f) o[e] = fmaf(__uint_as_float(x0[e]), w1, o[e]);
           }
-          if (mine) {
-            if (f32) {
+          if (f32) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(of + j + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            } else {
+            for (int e = 0; e < 8; ++e) st_shared4(stage + lane * 128 + ((e ^ (lane & 7)) << 4), o + 4 * e);
+            __syncwarp();
 #pragma unroll
-              for (int e = 0; e < 32; e += 8)
-                *reinterpret_cast<uint4*>(ob + j + e) =
-                    make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
-                               pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+            for (int i = 0; i < 8; ++i) {  // 8 lanes a row
+              const int r = 4 * i + (lane >> 3), e = lane & 7;
+              const int64_t to = __shfl_sync(0xffffffffu, off, r);
+              const float4 v = ld_shared4(stage + r * 128 + ((e ^ (r & 7)) << 4));
+              if (to >= 0) *reinterpret_cast<float4*>(of + to + j + 4 * e) = v;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint4 pk = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                                          pack_bf16x2(o[8 * e + 4], o[8 * e + 5]),
+                                          pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+              st_shared4(stage + lane * 64 + ((e ^ (lane >> 1 & 3)) << 4), reinterpret_cast<const float*>(&pk));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // 4 lanes a row
+              const int r = 8 * i + (lane >> 2), e = lane & 3;
+              const int64_t to = __shfl_sync(0xffffffffu, off, r);
+              const float4 v = ld_shared4(stage + r * 64 + ((e ^ (r >> 1 & 3)) << 4));
+              if (to >= 0) *reinterpret_cast<float4*>(ob + to + j + 8 * e) = v;
             }
           }
         }
@@ -830,7 +901,7 @@ int tree_ctas(int B, int64_t R, int H, int Hk, int page, int max_pages) {
   const int64_t sms = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
   const int64_t nodes = R < kMaxNodes ? R : kMaxNodes;
   const int64_t seqs = B < R ? B : R;  // with a node
-  const int64_t items = Hk * (seqs + R * (H / Hk) / kItemRows);
+  const int64_t items = Hk * (seqs + R * (H / Hk) / kTile);  // row tiles
   const int64_t tiles = ceil_div((int64_t)max_pages * page, kTile) + (nodes > 0 ? 1 : 0);
   const int64_t most = items * tiles / kMinShare;
   return (int)(most < 1 ? 1 : most < sms ? most : sms);

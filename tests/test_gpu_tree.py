@@ -246,6 +246,34 @@ def test_repeats_and_captured_calls_follow_new_lengths(csa):
     assert csa.csa_check_status(ws) == 0
 
 
+def test_many_items_a_share(csa):
+    """Shares of several items whose last row tiles are filled in part, back to back."""
+    x = make([2052, 1930], [47, 53], 32, 8, 128, 64, seed=17)
+    first = None
+    for _ in range(6):
+        O, lse, _ = call(csa, x)
+        first = O if first is None else first
+        assert torch.equal(O, first)
+    check(x, O, lse)
+
+
+@pytest.mark.parametrize("H,Hk,d,page", [(64, 1, 128, 128), (28, 4, 64, 32)])
+def test_short_sequences_back_to_back(csa, H, Hk, d, page):
+    """Items of one or two key tiles, whose products finish before the outputs of the
+    item before are written: the roles of a CTA may drift apart as far as they can."""
+    g = torch.Generator().manual_seed(18)
+    lens = torch.randint(0, 150, (90,), generator=g).tolist()
+    nodes = torch.randint(1, 9, (90,), generator=g).tolist()
+    x = make(lens, nodes, H, Hk, d, page, seed=19)
+    c = {k: v.cuda() for k, v in x.items()}
+    O, lse, ws = call(csa, x)
+    check(x, O, lse)
+    for _ in range(40):
+        again, _, _ = csa.csa_tree_attn(c["q"], c["Kp"], c["Vp"], c["table"], c["lens"], c["start"], c["mask"],
+                                        1 / math.sqrt(d), pos=c["pos"], workspace=ws)
+    assert torch.equal(again, O) and csa.csa_check_status(ws) == 0
+
+
 def test_empty_calls(csa):
     x = make([10], [2], 4, 1, 64, 16)
     x["start"] = torch.zeros(2, dtype=torch.int32)   # rows, but no nodes
