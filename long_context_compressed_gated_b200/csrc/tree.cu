@@ -110,6 +110,46 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// Packed fp32 pairs (per component the scalar IEEE operation).
+__device__ __forceinline__ unsigned long long pair_bits(float2 a) {
+  unsigned long long x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  return x;
+}
+__device__ __forceinline__ float2 bits_pair(unsigned long long x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long z;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(z) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+  return bits_pair(z);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long z;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(z) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return bits_pair(z);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// 2^x of two arguments on the fma pipe: x = n + f with n the nearest whole number
+// (added to 1.5 * 2^23, whose last bit is 1), |f| <= 1/2, a polynomial of degree 4
+// for 2^f (least-squares fit to equal relative error, 2.7e-6) and n added to the
+// exponent.  Arguments below -126 give 2^-126, not 0: only for tiles without masks.
+constexpr int kPolyPairs = 1;
+__device__ __forceinline__ float2 poly_exp2(float2 x) {
+  x.x = fmaxf(x.x, -126.f), x.y = fmaxf(x.y, -126.f);
+  const float2 t = add2(x, both(12582912.f));
+  const float2 f = add2(x, add2(both(12582912.f), make_float2(-t.x, -t.y)));
+  float2 p = fma2(f, both(9.5701003e-3f), both(5.5917859e-2f));
+  p = fma2(p, f, both(2.4024744e-1f));
+  p = fma2(p, f, both(6.9312179e-1f));
+  p = fma2(p, f, both(9.9999928e-1f));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+
 __device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b, bool tell) {
   Seq q;
   q.r0 = a.q_start[b];
@@ -225,15 +265,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::off_bar);
   uint64_t* kv_full = bar;                  // [kStages] tile landed
   uint64_t* kv_empty = bar + kStages;       // [kStages] its products complete
-  uint64_t* q_full = bar + 2 * kStages;     // [2] row tile in shared memory
-  uint64_t* s_full = bar + 2 * kStages + 2;   // [2] S of a stream's tile complete
-  uint64_t* p_full = bar + 2 * kStages + 4;   // [2] P written
-  uint64_t* o_full = bar + 2 * kStages + 6;   // [2] a stream's last PV of a segment complete
-  uint64_t* o_free = bar + 2 * kStages + 8;   // the segment's outputs read out of TMEM
-  uint64_t* seg_full = bar + 2 * kStages + 9;  // [2] a segment's description is in its slot
-  uint64_t* seg_free = bar + 2 * kStages + 11;  // [2] every role is done with the slot
-  uint64_t* mma_fin = bar + 2 * kStages + 13;
-  uint64_t* ex_full = bar + 2 * kStages + 14;   // statistics of merging streams: written, then read
+  uint64_t* q_full = bar + 2 * kStages;        // [2] row tile in shared memory
+  uint64_t* s_full = bar + 2 * kStages + 2;    // [2] S of a stream's tile complete
+  uint64_t* p_full = bar + 2 * kStages + 4;    // [2][2] P of a stream's tile written: keys 0..63, 64..127
+  uint64_t* o_full = bar + 2 * kStages + 8;    // [2] a stream's last PV of a segment complete
+  uint64_t* o_free = bar + 2 * kStages + 10;   // the segment's outputs read out of TMEM
+  uint64_t* seg_full = bar + 2 * kStages + 11;  // [2] a segment's description is in its slot
+  uint64_t* seg_free = bar + 2 * kStages + 13;  // [2] every role is done with the slot
+  uint64_t* mma_fin = bar + 2 * kStages + 15;  // every product complete
+  uint64_t* ex_full = bar + 2 * kStages + 16;  // statistics of merging streams: written, then read
   uint8_t* s_seg = smem + L::off_seg;
   int* misc = reinterpret_cast<int*>(smem + L::off_misc);  // [0] tmem
   volatile int* s_abort = misc + 1;  // set by the first wait that timed out; every role then stops
@@ -249,13 +289,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 4);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[2 * i], 4);
+      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_full[i], 1);
       mbar_init(&seg_full[i], 1);
       mbar_init(&seg_free[i], kSoftmaxWarps + 1);
     }
-    mbar_init(o_free, kSoftmaxWarps);
     mbar_init(mma_fin, 1);
+    mbar_init(o_free, kSoftmaxWarps);
     mbar_init(ex_full, kSoftmaxWarps);
     *s_abort = 0;
     fence_mbar_init();
@@ -444,40 +485,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     // operand descriptors of the first row tile, of a K and of a V tile in stage 0; other
     // places are added to the address field (16-byte units)
     const uint32_t skv = smem_u32(s_kv);
+    constexpr uint32_t kTile16 = L::kTileBytes / 16;
     const uint64_t q_desc = make_sdesc(smem_u32(s_q), 16, 1024, kSwizzle128);
     const uint64_t k_desc = make_sdesc(skv, 16, 1024, kSwizzle128);
     const uint64_t v_desc = make_sdesc(skv, kHalfBytes, 1024, kSwizzle128);
-    constexpr uint32_t kTile16 = L::kTileBytes / 16;
     bool live = true;
     int loads = 0;   // ring position of the segment's first tile
     int duals = 0;   // segments so far that loaded a second row tile
-    uint32_t steps = 0xFFu;    // steps of 16 keys of the current V tile that some row sees
-    int jobs0 = 0, jobs1 = 0;  // tiles so far of the two streams: the phases of their P barriers
+    uint32_t phases = 0;  // of the P barriers: bit st the parity of stream st's next tile
     for (int n = 0; live; ++n) {
       const Segment* sp = next_segment(n);
       if (sp == nullptr) break;
       const Segment& s = *sp;
       const bool dual = s.rows > kTile;
-      const int nt = s.t1 - s.t0;
+      const int nt = s.t1 - s.t0, t0 = s.t0;
       const int jobs = dual ? 2 * nt : nt;  // job x: stream x & 1, key tile dual ? x / 2 : x
+      // tiles [whole0, whole1) of the segment have no hidden row
+      const int whole0 = (int)(ceil_div(s.lo, kTile) - t0), whole1 = (int)(s.L / kTile - t0);
       if (!wait(&q_full[0], (uint32_t)(n & 1)) || (dual && !wait(&q_full[1], (uint32_t)(duals & 1)))) break;
       if (dual) ++duals;
-      tc_fence_after();
+      // S = Q K^T of job x; the K tile is free after the last stream's
       auto issue_s = [&](int x) -> bool {
         const int st = x & 1, t = dual ? x >> 1 : x;
-        const int at = loads + k_place(dual, t);
-        if (!(dual && st) && !wait(&kv_full[at % kStages], (uint32_t)((at / kStages) & 1))) return false;
+        const int at = loads + k_place(dual, t), sg = at % kStages;
+        if (!(dual && st) && !wait(&kv_full[sg], (uint32_t)((at / kStages) & 1))) return false;
         tc_fence_after();
         if (elect_one()) {
           const uint64_t qd = q_desc + (dual && st ? kTile16 : 0u);
-          const uint64_t kd = k_desc + (uint32_t)(at % kStages) * kTile16;
+          const uint64_t kd = k_desc + (uint32_t)sg * kTile16;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16;
             mma_bf16_ss(tbase + kTmemS + st * 128, qd + off, kd + off, idesc_bf16(128, kTile, 0, 0), kk > 0);
           }
           mma_commit(&s_full[st]);
-          if (!dual || st) mma_commit(&kv_empty[at % kStages]);
+          if (!dual || st) mma_commit(&kv_empty[sg]);
         }
         __syncwarp();
         return true;
@@ -485,26 +527,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       live = issue_s(0) && (jobs < 2 || issue_s(1));
       // the outputs of the segment before must be out of TMEM before the first PV
       if (live && n > 0) live = wait(o_free, (uint32_t)((n - 1) & 1));
-      tc_fence_after();
+      uint32_t steps = 0xFFu;  // steps of 16 keys of the current V tile that some row sees
       for (int x = 0; x < jobs && live; ++x) {
         const int st = x & 1, t = dual ? x >> 1 : x;
-        const int at = loads + v_place(dual, t, nt);
-        if (!wait(&p_full[st], (uint32_t)((st ? jobs1++ : jobs0++) & 1))) {
-          live = false;
-          break;
-        }
+        const int at = loads + v_place(dual, t, nt), sg = at % kStages;
         if (!(dual && st)) {
-          if (!wait(&kv_full[at % kStages], (uint32_t)((at / kStages) & 1))) {
+          if (!wait(&kv_full[sg], (uint32_t)((at / kStages) & 1))) {
             live = false;
             break;
           }
           // Rows that no node sees hold anything (or were not fetched).  Sixteen keys are one
           // step of the product: steps without a visible row are left out, the hidden rows of
           // the others zeroed.
-          const int64_t k0 = (int64_t)(s.t0 + t) * kTile;
           steps = 0xFFu;
-          if (k0 < s.lo || k0 + kTile > s.L) {
-            const uint32_t seen = visible(k0 + 16 * (lane & 7), s.lo, s.L, s.any) & 0xFFFFu;
+          if (t < whole0 || t >= whole1) {
+            const uint32_t seen =
+                visible((int64_t)(t0 + t) * kTile + 16 * (lane & 7), s.lo, s.L, s.any) & 0xFFFFu;
             steps = __ballot_sync(0xffffffffu, seen != 0) & 0xFFu;
             if (steps == 0) steps = 1;  // (a segment without any visible row still writes its output)
             uint32_t mend = __ballot_sync(0xffffffffu, seen != 0xFFFFu) & steps;
@@ -512,8 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int ks = __ffs(mend) - 1;
               mend &= mend - 1;
               if (!(__shfl_sync(0xffffffffu, seen, ks) >> (lane >> 1) & 1)) {
-                const uint32_t row = skv + (uint32_t)(at % kStages) * L::kTileBytes +
-                                     (uint32_t)(16 * ks + (lane >> 1)) * 128 + (uint32_t)(lane & 1) * 64;
+                const uint32_t row = skv + (uint32_t)sg * L::kTileBytes + (uint32_t)(16 * ks + (lane >> 1)) * 128 +
+                                     (uint32_t)(lane & 1) * 64;
 #pragma unroll
                 for (int i = 0; i < 4 * HALVES; ++i)
                   asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + (i >> 2) * kHalfBytes +
@@ -526,22 +564,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
         }
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t pcol = tbase + kTmemS + st * 128, o = tbase + kTmemO + st * D;
-          const uint64_t vd = v_desc + (uint32_t)(at % kStages) * kTile16;
+        // O += P V, the first 64 keys as soon as their P is written
+        const uint64_t vd = v_desc + (uint32_t)sg * kTile16;
+        const uint32_t t_s = tbase + kTmemS + st * 128, t_o = tbase + kTmemO + st * D;
 #pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            if (steps >> ks & 1)
-              mma_bf16_ts(o, pcol + 8 * ks, vd + ks * 128, idesc_bf16(128, D, 0, 1),
-                          (x >= 2 || (steps & ((1u << ks) - 1))) ? 1u : 0u);
-          if (!dual || st) mma_commit(&kv_empty[at % kStages]);
-          if (x + 2 >= jobs) mma_commit(&o_full[st]);
+        for (int h = 0; h < 2; ++h) {
+          if (!wait(&p_full[2 * st + h], phases >> st & 1)) {
+            live = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+              if (steps >> ks & 1)
+                mma_bf16_ts(t_o, t_s + 8 * ks, vd + ks * 128, idesc_bf16(128, D, 0, 1),
+                            (x >= 2 || (steps & ((1u << ks) - 1))) ? 1u : 0u);
+            if (h == 1) {
+              if (!dual || st) mma_commit(&kv_empty[sg]);
+              if (x + 2 >= jobs) mma_commit(&o_full[st]);
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        if (x + 2 < jobs && !issue_s(x + 2)) live = false;
+        phases ^= 1u << st;
+        if (live && x + 2 < jobs) live = issue_s(x + 2);
       }
-      if (jobs == 1) {  // the second stream had nothing: its barrier keeps step
+      if (live && jobs == 1) {  // the second stream had nothing: its barrier keeps step
         if (elect_one()) mma_commit(&o_full[1]);
         __syncwarp();
       }
@@ -625,25 +674,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         tc_fence_after();
         if (warp_mine) {
+          // raw logits of the row, 128 columns; the maximum of the first half while the second lands
           uint32_t v[kTile];
-#pragma unroll
-          for (int j = 0; j < kTile; j += 32) tmem_ld32p(scol + j, v + j);
-          tmem_wait_ld_regs32(v);
-#pragma unroll
-          for (int j = 32; j < kTile; j += 32) tmem_tie32(v + j);
-          // columns out of sight become -inf
-          if (__any_sync(0xffffffffu, !(lo <= base && base + kTile <= s.L))) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t bits = visible(base + 32 * w, lo, s.L, mask);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(bits >> e & 1)) v[32 * w + e] = 0xFF800000u;
-            }
-          }
+          const bool all = __all_sync(0xffffffffu, lo <= base && base + kTile <= s.L);  // no mask in this tile
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          tmem_ld32p(scol, v);
+          tmem_ld32p(scol + 32, v + 32);
+          tmem_wait_ld_regs32(v);
+          tmem_tie32(v + 32);
+          tmem_ld32p(scol + 64, v + 64);
+          tmem_ld32p(scol + 96, v + 96);
 #pragma unroll
-          for (int e = 0; e < kTile; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1) {
+              tmem_wait_ld_regs32(v + 64);
+              tmem_tie32(v + 96);
+            }
+            if (!all) {  // columns out of sight become -inf
+#pragma unroll
+              for (int w = 2 * h; w < 2 * h + 2; ++w) {
+                const uint32_t bits = visible(base + 32 * w, lo, s.L, mask);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!(bits >> e & 1)) v[32 * w + e] = 0xFF800000u;
+              }
+            }
+#pragma unroll
+            for (int e = 64 * h; e < 64 * h + 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
+          }
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
           const bool raise = mt > m_run + kRescaleSlack || (m_run == -INFINITY && mt > -INFINITY);
           const float m_new = raise ? mt : m_run;
@@ -664,24 +722,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           m_run = m_new;
           // p = 2^(s c - m); the sums take the unrounded weights, the product with V
-          // their bf16 rounding (the tensor pipe's operand type)
+          // their bf16 rounding (the tensor pipe's operand type).  Of every eight weights
+          // of an unmasked tile kPolyPairs pairs go to the fma pipe, the rest to the SFU.
 #pragma unroll
-          for (int j = 0; j < kTile; j += 64) {
+          for (int h = 0; h < 2; ++h) {
             uint32_t pk[32];
+            if (all) {
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-              const float p0 = fast_exp2(fmaf(__uint_as_float(v[j + e]), c, -m_use));
-              const float p1 = fast_exp2(fmaf(__uint_as_float(v[j + e + 1]), c, -m_use));
-              l2.x += p0, l2.y += p1;
-              pk[e / 2] = pack_bf16x2(p0, p1);
+              for (int e = 0; e < 64; e += 2) {
+                float2 z = fma2(make_float2(__uint_as_float(v[64 * h + e]), __uint_as_float(v[64 * h + e + 1])),
+                                make_float2(c, c), make_float2(-m_use, -m_use));
+                if ((e & 7) >= 8 - 2 * kPolyPairs) z = poly_exp2(z);
+                else z.x = fast_exp2(z.x), z.y = fast_exp2(z.y);
+                l2 = add2(l2, z);
+                pk[e / 2] = pack_bf16x2(z.x, z.y);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 64; e += 2) {
+                float2 z = fma2(make_float2(__uint_as_float(v[64 * h + e]), __uint_as_float(v[64 * h + e + 1])),
+                                make_float2(c, c), make_float2(-m_use, -m_use));
+                z.x = fast_exp2(z.x), z.y = fast_exp2(z.y);
+                l2 = add2(l2, z);
+                pk[e / 2] = pack_bf16x2(z.x, z.y);
+              }
             }
-            tmem_st32p(scol + j / 2, pk);
+            tmem_st32p(scol + 32 * h, pk);
+            if (h == 0) {
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&p_full[2 * st]);
+            }
           }
           tmem_wait_st();
+        } else if (lane == 0) {
+          mbar_arrive(&p_full[2 * st]);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[st]);
+        if (lane == 0) mbar_arrive(&p_full[2 * st + 1]);
       }
       // ---- outputs
       if (!live || !wait(&o_full[st], (uint32_t)(n & 1))) break;
@@ -718,8 +798,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* of = part ? a.part_o : static_cast<float*>(a.O);
       __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.O);
       const int c0 = !dual && st ? D / 2 : 0, c1 = !dual && !st ? D / 2 : D;
-      const bool both = !dual;
-      const float w0 = both || st == 0 ? f[0] : f[1], w1 = both ? f[1] : 0.f;
+      const bool merge = !dual;
+      const float w0 = merge || st == 0 ? f[0] : f[1], w1 = merge ? f[1] : 0.f;
       if (warp_mine) {
         const uint32_t stage = smem_u32(s_q) + (uint32_t)(st * L::kTileBytes + (warp & 3) * 32 * 128);
 #pragma unroll 1
@@ -727,12 +807,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t x0[32];
           float o[32];
           __syncwarp();  // (the pieces staged before have been read)
-          tmem_ld32p(lane_base + kTmemO + (both ? 0 : st * D) + j, x0);
+          tmem_ld32p(lane_base + kTmemO + (merge ? 0 : st * D) + j, x0);
           tmem_wait_ld_regs32(x0);
           // an accumulator without a key holds no data: weight 0 exactly
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = w0 != 0.f ? __uint_as_float(x0[e]) * w0 : 0.f;
-          if (both) {
+          if (merge) {
             tmem_ld32p(lane_base + kTmemO + D + j, x0);
             tmem_wait_ld_regs32(x0);
 #pragma unroll
