@@ -231,6 +231,18 @@ __device__ __forceinline__ float4 ld_shared4(uint32_t addr) {
   return v;
 }
 
+// A value that is the same in every lane, said so that the compiler may keep it (and
+// what follows from it, operand descriptors above all) in uniform registers.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Shared-memory descriptor from the halves that make_sdesc builds: the high one is a
+// constant of the layout, places are added to the low one.
+__device__ __forceinline__ uint64_t sdesc(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+
 // Bits [lo, hi) of a 32-bit word (lo and hi anything).
 __device__ __forceinline__ uint32_t bit_range(int64_t lo, int64_t hi) {
   if (lo < 0) lo = 0;
@@ -489,6 +501,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t q_desc = make_sdesc(smem_u32(s_q), 16, 1024, kSwizzle128);
     const uint64_t k_desc = make_sdesc(skv, 16, 1024, kSwizzle128);
     const uint64_t v_desc = make_sdesc(skv, kHalfBytes, 1024, kSwizzle128);
+    const uint32_t q_lo = (uint32_t)q_desc, qk_hi = (uint32_t)(k_desc >> 32);
+    const uint32_t k_lo = (uint32_t)k_desc, v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32);
+    const uint32_t tmem = (uint32_t)uniform((int)tbase);
     bool live = true;
     int loads = 0;   // ring position of the segment's first tile
     int duals = 0;   // segments so far that loaded a second row tile
@@ -497,11 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Segment* sp = next_segment(n);
       if (sp == nullptr) break;
       const Segment& s = *sp;
-      const bool dual = s.rows > kTile;
-      const int nt = s.t1 - s.t0, t0 = s.t0;
+      const bool dual = uniform(s.rows) > kTile;
+      const int t0 = uniform(s.t0), nt = uniform(s.t1) - t0;
       const int jobs = dual ? 2 * nt : nt;  // job x: stream x & 1, key tile dual ? x / 2 : x
       // tiles [whole0, whole1) of the segment have no hidden row
-      const int whole0 = (int)(ceil_div(s.lo, kTile) - t0), whole1 = (int)(s.L / kTile - t0);
+      const int whole0 = uniform((int)ceil_div(s.lo, kTile)) - t0, whole1 = uniform((int)(s.L / kTile)) - t0;
       if (!wait(&q_full[0], (uint32_t)(n & 1)) || (dual && !wait(&q_full[1], (uint32_t)(duals & 1)))) break;
       if (dual) ++duals;
       // S = Q K^T of job x; the K tile is free after the last stream's
@@ -511,12 +526,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(dual && st) && !wait(&kv_full[sg], (uint32_t)((at / kStages) & 1))) return false;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t qd = q_desc + (dual && st ? kTile16 : 0u);
-          const uint64_t kd = k_desc + (uint32_t)sg * kTile16;
+          const uint32_t qd = q_lo + (dual && st ? kTile16 : 0u), kd = k_lo + (uint32_t)sg * kTile16;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16;
-            mma_bf16_ss(tbase + kTmemS + st * 128, qd + off, kd + off, idesc_bf16(128, kTile, 0, 0), kk > 0);
+            mma_bf16_ss(tmem + kTmemS + st * 128, sdesc(qd + off, qk_hi), sdesc(kd + off, qk_hi),
+                        idesc_bf16(128, kTile, 0, 0), kk > 0);
           }
           mma_commit(&s_full[st]);
           if (!dual || st) mma_commit(&kv_empty[sg]);
@@ -565,8 +580,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // O += P V, the first 64 keys as soon as their P is written
-        const uint64_t vd = v_desc + (uint32_t)sg * kTile16;
-        const uint32_t t_s = tbase + kTmemS + st * 128, t_o = tbase + kTmemO + st * D;
+        const uint32_t vd = v_lo + (uint32_t)sg * kTile16;
+        const uint32_t t_s = tmem + kTmemS + st * 128, t_o = tmem + kTmemO + st * D;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (!wait(&p_full[2 * st + h], phases >> st & 1)) {
@@ -575,11 +590,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           if (elect_one()) {
+            if (steps == 0xFFu) {
 #pragma unroll
-            for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-              if (steps >> ks & 1)
-                mma_bf16_ts(t_o, t_s + 8 * ks, vd + ks * 128, idesc_bf16(128, D, 0, 1),
-                            (x >= 2 || (steps & ((1u << ks) - 1))) ? 1u : 0u);
+              for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                mma_bf16_ts(t_o, t_s + 8 * ks, sdesc(vd + ks * 128, v_hi), idesc_bf16(128, D, 0, 1),
+                            ks > 0 ? 1u : x >= 2);
+            } else {
+#pragma unroll 1
+              for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                if (steps >> ks & 1)
+                  mma_bf16_ts(t_o, t_s + 8 * ks, sdesc(vd + ks * 128, v_hi), idesc_bf16(128, D, 0, 1),
+                              (x >= 2 || (steps & ((1u << ks) - 1))) ? 1u : 0u);
+            }
             if (h == 1) {
               if (!dual || st) mma_commit(&kv_empty[sg]);
               if (x + 2 >= jobs) mma_commit(&o_full[st]);
