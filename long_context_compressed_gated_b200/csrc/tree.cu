@@ -41,6 +41,7 @@
 #include <cudaTypedefs.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "checks.cuh"
 #include "sm100.cuh"
@@ -95,9 +96,9 @@ struct TreeArgs {
 // What one sequence asks for.
 struct Seq {
   int r0, n;        // first row of the call, nodes
-  int64_t L, S;     // committed rows, all rows
-  int64_t lo;       // first row that any node may see
-  int64_t tile0;    // first key tile
+  int L, S;         // committed rows, all rows (max_pages * page < 2^31 - 128)
+  int lo;           // first row that any node may see
+  int tile0;        // first key tile
   int tiles;        // key tiles (one at least: an item without keys still writes its rows)
   int units;        // row tiles per key head: ceil(n * G / 128)
   __device__ int64_t total(int Hk) const { return (int64_t)tiles * units * Hk; }
@@ -107,6 +108,12 @@ struct Seq {
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 
@@ -133,21 +140,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// 2^x of two arguments on the fma pipe: x = n + f with n the nearest whole number
-// (added to 1.5 * 2^23, whose last bit is 1), |f| <= 1/2, a polynomial of degree 4
-// for 2^f (least-squares fit to equal relative error, 2.7e-6) and n added to the
-// exponent.  Arguments below -126 give 2^-126, not 0: only for tiles without masks.
-constexpr int kPolyPairs = 1;
-__device__ __forceinline__ float2 poly_exp2(float2 x) {
-  x.x = fmaxf(x.x, -126.f), x.y = fmaxf(x.y, -126.f);
-  const float2 t = add2(x, both(12582912.f));
-  const float2 f = add2(x, add2(both(12582912.f), make_float2(-t.x, -t.y)));
-  float2 p = fma2(f, both(9.5701003e-3f), both(5.5917859e-2f));
-  p = fma2(p, f, both(2.4024744e-1f));
-  p = fma2(p, f, both(6.9312179e-1f));
-  p = fma2(p, f, both(9.9999928e-1f));
-  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+// The first committed row that a node at position pos sees (pos may be anything).
+__device__ __forceinline__ int window_start(int64_t pos, int W, int L) {
+  if (pos < W) return 0;  // pos - W + 1 would be at most 0, or not fit
+  return pos - W + 1 > L ? L : (int)(pos - W + 1);
 }
 
 __device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b, bool tell) {
@@ -156,9 +152,10 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b, bool tell) {
   const int r1 = a.q_start[b + 1];
   q.L = a.lens[b];
   q.n = r1 - q.r0;
-  q.S = q.L + q.n;
+  q.S = 0;
   q.lo = 0;
-  if (q.r0 < 0 || q.n < 0 || r1 > a.R || q.L < 0 || q.n > kMaxNodes || q.S > ((int64_t)a.max_pages << a.page_shift)) {
+  if (q.r0 < 0 || q.n < 0 || r1 > a.R || q.L < 0 || q.n > kMaxNodes ||
+      (int64_t)q.L + q.n > ((int64_t)a.max_pages << a.page_shift)) {
     if (tell) report(a.status, CSA_ERR_INDEX);
     q.n = 0;
   }
@@ -167,22 +164,24 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b, bool tell) {
     q.tile0 = 0;
     return q;
   }
+  q.S = q.L + q.n;
   if (a.W >= 0) {
     int64_t p = a.pos[q.r0];
-#pragma unroll 8
+#pragma unroll 2
     for (int i = 1; i < q.n; ++i) {
       const int64_t x = a.pos[q.r0 + i];
       p = x < p ? x : p;
     }
-    q.lo = p - a.W + 1;
-    q.lo = q.lo < 0 ? 0 : q.lo > q.L ? q.L : q.lo;
+    q.lo = window_start(p, a.W, q.L);
   }
   q.tile0 = q.lo / kTile;
-  q.tiles = (int)ceil_div(q.S - q.tile0 * kTile, kTile);
+  q.tiles = (q.S - q.tile0 * kTile + kTile - 1) / kTile;
   if (q.tiles < 1) q.tiles = 1;
   q.units = (int)ceil_div((int64_t)q.n * a.G, kTile);
   return q;
 }
+
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) { return a / b; }
 
 // One segment of a share: part of one item.
 struct Segment {
@@ -191,8 +190,7 @@ struct Segment {
   int row0, rows;     // the item's first (node, head) row and its rows
   int hk;
   int t0, t1;         // its key tiles, counted from tile 0 of the sequence
-  int64_t L, lo;
-  uint64_t any;       // drafted rows that some node sees
+  int L, lo;
   int slot;           // partial result slot, or -1: the whole item, final
 };
 
@@ -209,14 +207,6 @@ struct TreeSmem {
   static constexpr size_t bytes = off_misc + 64 + 1024;
 };
 static_assert(sizeof(Segment) <= 128, "segment slot");
-
-// Position of K / V of key tile t of a segment of n tiles in its stream of loads:
-// the order in which the MMA warp uses them.  Both streams on every tile:
-// K0 V0 K1 V1 ..; alternate tiles: K0 K1 V0 K2 V1 .. (S runs one tile ahead).
-__device__ __forceinline__ int k_place(bool dual, int t) { return dual ? 2 * t : (t == 0 ? 0 : 2 * t - 1); }
-__device__ __forceinline__ int v_place(bool dual, int t, int n) {
-  return dual ? 2 * t + 1 : (t == n - 1 ? 2 * n - 1 : 2 * t + 2);
-}
 
 __device__ __forceinline__ void st_shared4(uint32_t addr, const float* v) {
   asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
@@ -244,17 +234,17 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t lo, uint32_t hi) {
 }
 
 // Bits [lo, hi) of a 32-bit word (lo and hi anything).
-__device__ __forceinline__ uint32_t bit_range(int64_t lo, int64_t hi) {
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   if (lo < 0) lo = 0;
   if (hi > 32) hi = 32;
   if (lo >= hi) return 0u;
-  return (0xFFFFFFFFu >> (32 - (int)(hi - lo))) << (int)lo;
+  return (0xFFFFFFFFu >> (32 - (hi - lo))) << lo;
 }
 
 // Visible columns off .. off+31 of a row: committed rows [lo, L), drafted rows by mask.
-__device__ __forceinline__ uint32_t visible(int64_t off, int64_t lo, int64_t L, uint64_t mask) {
+__device__ __forceinline__ uint32_t visible(int off, int lo, int L, uint64_t mask) {
   uint32_t w = bit_range(lo - off, L - off);
-  const int64_t sh = off - L;
+  const int sh = off - L;
   if (sh >= 0) {
     if (sh < 64) w |= (uint32_t)(mask >> sh);
   } else if (sh > -32) {
@@ -327,9 +317,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Bounded wait that also stops once any role of this CTA has given up.
   auto wait = [&](uint64_t* b_, uint32_t ph) -> bool {
     if (mbar_try_wait(b_, ph)) return true;
-    if (*s_abort) return false;
-    if (mbar_wait(b_, ph, a.status, CSA_ERR_DEVICE_TIMEOUT)) return true;
-    *s_abort = 1;
+    const long long start = clock64();
+    while (!*s_abort) {
+      if (mbar_try_wait(b_, ph)) return true;
+      if (clock64() - start > CSA_WAIT_CYCLES) {
+        report(a.status, CSA_ERR_DEVICE_TIMEOUT);
+        *s_abort = 1;
+      }
+    }
     return false;
   };
   // the next segment's description (in place until the role releases it), or null
@@ -347,26 +342,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_decrease<kOtherRegs>();
     // =========================== the share: its segments and their K / V tiles
     griddep_launch_dependents();
-    // total key tiles; which sequence the share starts in (every lane a stride of
-    // sequences, then the same in order)
+    // what every sequence asks for, 32 of them at a time (lane: sequence block + lane); the
+    // sum over all first, then the sequence that holds the share's first position
     const bool skip = *reinterpret_cast<volatile int*>(a.status) == CSA_ERR_DEVICE_TIMEOUT;
-    int64_t total = 0;
-    for (int b = lane; b < a.B; b += 32) total += load_seq(a, b, blockIdx.x == 0).total(a.Hk);
+    int block = 0;
+    Seq mine = lane < a.B ? load_seq(a, lane, blockIdx.x == 0) : Seq{};
+    int64_t total = mine.total(a.Hk);
+#pragma unroll 1
+    for (int b = 32 + lane; b < a.B; b += 32) total += load_seq(a, b, blockIdx.x == 0).total(a.Hk);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     int64_t ctas = total / kMinShare;
     ctas = ctas < 1 ? 1 : ctas > gridDim.x ? gridDim.x : ctas;
     const int64_t c = blockIdx.x;
-    int64_t first = c < ctas ? c * total / ctas : 0, last = c < ctas ? (c + 1) * total / ctas : 0;
+    int64_t first = c < ctas ? div64(c * total, ctas) : 0, last = c < ctas ? div64((c + 1) * total, ctas) : 0;
     if (skip) first = last = 0;
     int4 split = make_int4(0, 0, 0, 0);
-    // find the sequence that holds tile `first`
     int b = 0;
-    int64_t at = 0;  // tiles before sequence b
+    int64_t at = 0;  // positions before sequence b
     if (first < last) {
-      for (int base = 0; base < a.B; base += 32) {
-        const int64_t mine = base + lane < a.B ? load_seq(a, base + lane, false).total(a.Hk) : 0;
-        int64_t up = mine;  // inclusive prefix
+      for (;;) {
+        int64_t up = mine.total(a.Hk);  // inclusive prefix
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int64_t y = __shfl_up_sync(0xffffffffu, up, o);
@@ -375,21 +371,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t over = __ballot_sync(0xffffffffu, at + up > first);
         if (over) {
           const int w = __ffs(over) - 1;
-          b = base + w;
-          at += __shfl_sync(0xffffffffu, up - mine, w);
+          b = block + w;
+          at += __shfl_sync(0xffffffffu, up - mine.total(a.Hk), w);
           break;
         }
         at += __shfl_sync(0xffffffffu, up, 31);
+        block += 32;
+        if (block >= a.B) break;
+        mine = block + lane < a.B ? load_seq(a, block + lane, false) : Seq{};
       }
     }
+    // sequence b (of the current block, or the first of the next)
+    auto sequence = [&](int b_) -> Seq {
+      if (b_ >= block + 32) {
+        block += 32;
+        mine = block + lane < a.B ? load_seq(a, block + lane, false) : Seq{};
+      }
+      const int w = b_ - block;
+      Seq q;
+      q.r0 = __shfl_sync(0xffffffffu, mine.r0, w);
+      q.n = __shfl_sync(0xffffffffu, mine.n, w);
+      q.L = __shfl_sync(0xffffffffu, mine.L, w);
+      q.S = __shfl_sync(0xffffffffu, mine.S, w);
+      q.lo = __shfl_sync(0xffffffffu, mine.lo, w);
+      q.tile0 = __shfl_sync(0xffffffffu, mine.tile0, w);
+      q.tiles = __shfl_sync(0xffffffffu, mine.tiles, w);
+      q.units = __shfl_sync(0xffffffffu, mine.units, w);
+      return q;
+    };
     int loads = 0;  // tiles fetched so far (ring position)
     int n = 0;      // segments published
     bool live = true;
+#pragma unroll 1
     for (int64_t g = first; g < last && live;) {
-      Seq q = load_seq(a, b, false);
+      Seq q = sequence(b);
       while (g >= at + q.total(a.Hk) && b + 1 < a.B) {
         at += q.total(a.Hk);
-        q = load_seq(a, ++b, false);
+        q = sequence(++b);
       }
       if (q.tiles == 0) break;
       // the item that holds position g: a key head's items of two row tiles, then perhaps
@@ -399,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       s.valid = 1;
       s.r0 = q.r0;
       s.n = q.n;
-      s.hk = (int)((g - at) / head);
-      const int set = (int)((g - at - s.hk * head) / (2 * q.tiles));
+      s.hk = (int)div64(g - at, head);
+      const int set = (int)div64(g - at - s.hk * head, 2 * q.tiles);
       s.row0 = set * kItemRows;
       const int left = q.n * a.G - s.row0;
       s.rows = left < kItemRows ? left : kItemRows;
@@ -408,23 +426,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t i0 = at + s.hk * head + (int64_t)set * 2 * q.tiles, i1 = i0 + (int64_t)wide * q.tiles;
       const int64_t end = i1 < last ? i1 : last;
       // a key tile goes to the share that holds its first position
-      const int t0 = (int)ceil_div(g - i0, wide), t1 = (int)ceil_div(end - i0, wide);
+      const int t0 = (int)((g - i0 + wide - 1) >> (wide - 1)), t1 = (int)((end - i0 + wide - 1) >> (wide - 1));
       g = end;
       if (t0 == t1) continue;
-      s.t0 = (int)q.tile0 + t0;
-      s.t1 = (int)q.tile0 + t1;
+      s.t0 = q.tile0 + t0;
+      s.t1 = q.tile0 + t1;
       s.L = q.L;
       s.lo = q.lo;
-      uint64_t any = 0;
-      for (int i = lane; i < q.n; i += 32) any |= a.mask[q.r0 + i];
-      s.any = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32 |
-              __reduce_or_sync(0xffffffffu, (uint32_t)any);
-      if (q.n < 64) s.any &= (1ull << q.n) - 1;
       s.slot = t0 == 0 && t1 == q.tiles ? -1 : (int)(2 * c) + (n == 0 ? 0 : 1);
       if (t0 == 0 && t1 < q.tiles) {  // the item goes on in the next CTAs: tell the combine
         const int64_t tail = i0 + (int64_t)wide * (q.tiles - 1);  // its last tile
-        int64_t cl = tail * ctas / total;
-        while ((cl + 1) * total / ctas <= tail) ++cl;
+        int64_t cl = div64(tail * ctas, total);
+        while (div64((cl + 1) * total, ctas) <= tail) ++cl;
         split = make_int4(s.rows, s.slot, (int)(cl - c + 1), 0);
         // first output row: (r0 * H + hk * G) and the item's rows from row0
         if (lane == 0) {
@@ -443,6 +456,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int box_rows = a.page_shift < 7 ? 1 << a.page_shift : kTile;
       const int boxes = kTile / box_rows * HALVES;  // per tile, at most 16
       const int my_row = lane / HALVES * box_rows, my_half = lane % HALVES;
+      // Page numbers are read ahead: lane l holds entries from + l and from + 32 + l of the
+      // sequence's table, one pair for K and one for V (which is up to two tiles behind)
+      const int32_t* table = a.table + (int64_t)b * a.max_pages;
+      const int last_page = (q.S - 1) >> a.page_shift;  // (a sequence with a node has S >= 1)
+      auto entry = [&](int p) { return p <= last_page ? table[p] : -1; };
+      const int from0 = (s.t0 * kTile) >> a.page_shift;
+      int from[2] = {from0, from0};
+      int now[2], next[2];
+      now[0] = now[1] = entry(from0 + lane);
+      next[0] = next[1] = entry(from0 + 32 + lane);
+#pragma unroll 1
       for (int i = 0; i < 2 * nt && live; ++i) {
         // load i of the segment: which tile of which kind
         int t, kind;
@@ -459,21 +483,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           live = false;
           break;
         }
-        const int64_t key = (int64_t)(s.t0 + t) * kTile + my_row;
+        const int key = (s.t0 + t) * kTile + my_row;
         const bool need = lane < boxes && key + box_rows > q.lo && key < q.S;
+        // (a tile's pages lie within one run of 32: both start at multiples of 128 keys)
         int page = 0;
-        if (need) {
-          page = a.table[(int64_t)b * a.max_pages + (key >> a.page_shift)];
-          if (page < 0 || page >= a.n_pages) {
-            report(a.status, CSA_ERR_INDEX);
-            page = a.n_pages > 0 ? (int)a.n_pages : 1;  // outside the map: zeros
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (kind != k) continue;
+          if (((s.t0 + t) * kTile) >> a.page_shift >= from[k] + 32) {
+            from[k] += 32;
+            now[k] = next[k];
+            next[k] = entry(from[k] + 32 + lane);
           }
+          page = __shfl_sync(0xffffffffu, now[k], ((key >> a.page_shift) - from[k]) & 31);
+        }
+        if (need && (page < 0 || page >= a.n_pages)) {
+          report(a.status, CSA_ERR_INDEX);
+          page = a.n_pages > 0 ? (int)a.n_pages : 1;  // outside the map: zeros
+        }
+        // at the start the query rows go first: behind a ring full of K and V they would
+        // wait for all of it
+        if (n == 0 && i == (dual || nt == 1 ? 1 : 2) &&
+            (!wait(&q_full[0], 0) || (dual && !wait(&q_full[1], 0)))) {
+          live = false;
+          break;
         }
         const int count = __popc(__ballot_sync(0xffffffffu, need));
         if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], (uint32_t)(count * box_rows * 128));
         __syncwarp();
         if (need) {
-          const int row = (s.hk << a.page_shift) + (int)(key & ((1 << a.page_shift) - 1));
+          const int row = (s.hk << a.page_shift) + (key & ((1 << a.page_shift) - 1));
           tma_load_3d(s_kv + (size_t)st * L::kTileBytes + my_half * kHalfBytes + my_row * 128,
                       kind ? &maps.v : &maps.k, &kv_full[st], my_half * 64, row, page);
         }
@@ -494,20 +533,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     regs_decrease<kOtherRegs>();
     // =========================== MMA issue
-    // operand descriptors of the first row tile, of a K and of a V tile in stage 0; other
-    // places are added to the address field (16-byte units)
+    // The tensor pipe runs dry whenever this warp's scalar work between two products is
+    // longer than the products that are queued, so the loop is kept short: streams and
+    // barriers are compile-time, ring stages counted, operand descriptors in uniform
+    // registers, and the issue predicated instead of branched.
     const uint32_t skv = smem_u32(s_kv);
     constexpr uint32_t kTile16 = L::kTileBytes / 16;
+    // descriptors of the first row tile, of a K and of a V tile in stage 0; other places are
+    // added to the address field (16-byte units)
     const uint64_t q_desc = make_sdesc(smem_u32(s_q), 16, 1024, kSwizzle128);
     const uint64_t k_desc = make_sdesc(skv, 16, 1024, kSwizzle128);
     const uint64_t v_desc = make_sdesc(skv, kHalfBytes, 1024, kSwizzle128);
     const uint32_t q_lo = (uint32_t)q_desc, qk_hi = (uint32_t)(k_desc >> 32);
     const uint32_t k_lo = (uint32_t)k_desc, v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32);
     const uint32_t tmem = (uint32_t)uniform((int)tbase);
+    const uint32_t leader = elect_one();
     bool live = true;
-    int loads = 0;   // ring position of the segment's first tile
-    int duals = 0;   // segments so far that loaded a second row tile
-    uint32_t phases = 0;  // of the P barriers: bit st the parity of stream st's next tile
+    int ring = 0;              // stage of the next K / V tile
+    uint32_t ring_phase = 0;   // and the parity of its barrier
+    uint32_t q1_phase = 0;     // parity of the second row tile's barrier
+    uint32_t p_phase[2] = {0, 0};
+    // the next tile of the ring, once it has landed: its stage, or -1
+    auto next_tile = [&]() -> int {
+      if (!wait(&kv_full[ring], ring_phase)) return -1;
+      const int st = ring;
+      if (++ring == kStages) ring = 0, ring_phase ^= 1;
+      return st;
+    };
+#pragma unroll 1
     for (int n = 0; live; ++n) {
       const Segment* sp = next_segment(n);
       if (sp == nullptr) break;
@@ -516,56 +569,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t0 = uniform(s.t0), nt = uniform(s.t1) - t0;
       const int jobs = dual ? 2 * nt : nt;  // job x: stream x & 1, key tile dual ? x / 2 : x
       // tiles [whole0, whole1) of the segment have no hidden row
-      const int whole0 = uniform((int)ceil_div(s.lo, kTile)) - t0, whole1 = uniform((int)(s.L / kTile)) - t0;
-      if (!wait(&q_full[0], (uint32_t)(n & 1)) || (dual && !wait(&q_full[1], (uint32_t)(duals & 1)))) break;
-      if (dual) ++duals;
-      // S = Q K^T of job x; the K tile is free after the last stream's
-      auto issue_s = [&](int x) -> bool {
-        const int st = x & 1, t = dual ? x >> 1 : x;
-        const int at = loads + k_place(dual, t), sg = at % kStages;
-        if (!(dual && st) && !wait(&kv_full[sg], (uint32_t)((at / kStages) & 1))) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t qd = q_lo + (dual && st ? kTile16 : 0u), kd = k_lo + (uint32_t)sg * kTile16;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16;
-            mma_bf16_ss(tmem + kTmemS + st * 128, sdesc(qd + off, qk_hi), sdesc(kd + off, qk_hi),
-                        idesc_bf16(128, kTile, 0, 0), kk > 0);
-          }
-          mma_commit(&s_full[st]);
-          if (!dual || st) mma_commit(&kv_empty[sg]);
-        }
+      const int whole0 = uniform((s.lo + kTile - 1) / kTile) - t0, whole1 = uniform(s.L / kTile) - t0;
+      // drafted rows that some node sees (used, and waited for, at the first tile with hidden rows)
+      const uint64_t seen_by = (lane < s.n ? a.mask[s.r0 + lane] : 0) | (lane + 32 < s.n ? a.mask[s.r0 + 32 + lane] : 0);
+      if (!wait(&q_full[0], (uint32_t)(n & 1)) || (dual && !wait(&q_full[1], q1_phase))) break;
+      if (dual) q1_phase ^= 1;
+      int ks = 0, vs = 0;      // stages of the K tile of the S to issue and of the V tile of the PV
+      uint32_t steps = 0xFFu;  // steps of 16 keys of that V tile that some row sees
+      // S = Q K^T; in a dual item the second stream's frees the K tile
+      auto issue_s = [&](auto stream) -> bool {
+        constexpr int st = decltype(stream)::value;
+        if (!(dual && st) && (ks = next_tile()) < 0) return false;
         __syncwarp();
+        tc_fence_after();
+        const uint32_t qd = q_lo + (dual && st ? kTile16 : 0u), kd = k_lo + (uint32_t)ks * kTile16;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16;
+          mma_bf16_ss_if(leader, tmem + kTmemS + st * 128, sdesc(qd + off, qk_hi), sdesc(kd + off, qk_hi),
+                         idesc_bf16(128, kTile, 0, 0), kk > 0);
+        }
+        mma_commit_if(leader, &s_full[st]);
+        if (!dual || st) mma_commit_if(leader, &kv_empty[ks]);
         return true;
       };
-      live = issue_s(0) && (jobs < 2 || issue_s(1));
-      // the outputs of the segment before must be out of TMEM before the first PV
-      if (live && n > 0) live = wait(o_free, (uint32_t)((n - 1) & 1));
-      uint32_t steps = 0xFFu;  // steps of 16 keys of the current V tile that some row sees
-      for (int x = 0; x < jobs && live; ++x) {
-        const int st = x & 1, t = dual ? x >> 1 : x;
-        const int at = loads + v_place(dual, t, nt), sg = at % kStages;
+      // job x: O += P V, the first 64 keys as soon as their P is written; then S of the stream's
+      // next tile over the same columns
+      auto job = [&](auto stream, int x) -> bool {
+        constexpr int st = decltype(stream)::value;
         if (!(dual && st)) {
-          if (!wait(&kv_full[sg], (uint32_t)((at / kStages) & 1))) {
-            live = false;
-            break;
-          }
-          // Rows that no node sees hold anything (or were not fetched).  Sixteen keys are one
-          // step of the product: steps without a visible row are left out, the hidden rows of
-          // the others zeroed.
+          if ((vs = next_tile()) < 0) return false;
+          const int t = dual ? x >> 1 : x;
           steps = 0xFFu;
           if (t < whole0 || t >= whole1) {
-            const uint32_t seen =
-                visible((int64_t)(t0 + t) * kTile + 16 * (lane & 7), s.lo, s.L, s.any) & 0xFFFFu;
+            // Rows that no node sees hold anything (or were not fetched).  Sixteen keys are one
+            // step of the product: steps without a visible row are left out, the hidden rows of
+            // the others zeroed.
+            const uint64_t any = ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(seen_by >> 32)) << 32 |
+                                  __reduce_or_sync(0xffffffffu, (uint32_t)seen_by)) &
+                                 (s.n < 64 ? (1ull << s.n) - 1 : ~0ull);
+            const uint32_t seen = visible((t0 + t) * kTile + 16 * (lane & 7), s.lo, s.L, any) & 0xFFFFu;
             steps = __ballot_sync(0xffffffffu, seen != 0) & 0xFFu;
             if (steps == 0) steps = 1;  // (a segment without any visible row still writes its output)
             uint32_t mend = __ballot_sync(0xffffffffu, seen != 0xFFFFu) & steps;
             while (mend != 0) {
-              const int ks = __ffs(mend) - 1;
+              const int k = __ffs(mend) - 1;
               mend &= mend - 1;
-              if (!(__shfl_sync(0xffffffffu, seen, ks) >> (lane >> 1) & 1)) {
-                const uint32_t row = skv + (uint32_t)sg * L::kTileBytes + (uint32_t)(16 * ks + (lane >> 1)) * 128 +
+              if (!(__shfl_sync(0xffffffffu, seen, k) >> (lane >> 1) & 1)) {
+                const uint32_t row = skv + (uint32_t)vs * L::kTileBytes + (uint32_t)(16 * k + (lane >> 1)) * 128 +
                                      (uint32_t)(lane & 1) * 64;
 #pragma unroll
                 for (int i = 0; i < 4 * HALVES; ++i)
@@ -579,49 +630,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
         }
-        // O += P V, the first 64 keys as soon as their P is written
-        const uint32_t vd = v_lo + (uint32_t)sg * kTile16;
-        const uint32_t t_s = tmem + kTmemS + st * 128, t_o = tmem + kTmemO + st * D;
+        const uint32_t vd = v_lo + (uint32_t)vs * kTile16;
+        constexpr uint32_t kS = kTmemS + st * 128, kO = kTmemO + st * D;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (!wait(&p_full[2 * st + h], phases >> st & 1)) {
-            live = false;
-            break;
-          }
-          tc_fence_after();
-          if (elect_one()) {
-            if (steps == 0xFFu) {
-#pragma unroll
-              for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-                mma_bf16_ts(t_o, t_s + 8 * ks, sdesc(vd + ks * 128, v_hi), idesc_bf16(128, D, 0, 1),
-                            ks > 0 ? 1u : x >= 2);
-            } else {
-#pragma unroll 1
-              for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-                if (steps >> ks & 1)
-                  mma_bf16_ts(t_o, t_s + 8 * ks, sdesc(vd + ks * 128, v_hi), idesc_bf16(128, D, 0, 1),
-                              (x >= 2 || (steps & ((1u << ks) - 1))) ? 1u : 0u);
-            }
-            if (h == 1) {
-              if (!dual || st) mma_commit(&kv_empty[sg]);
-              if (x + 2 >= jobs) mma_commit(&o_full[st]);
-            }
-          }
+          if (!wait(&p_full[2 * st + h], p_phase[st])) return false;
           __syncwarp();
+          tc_fence_after();
+          if (steps == 0xFFu) {
+#pragma unroll
+            for (int k = 4 * h; k < 4 * h + 4; ++k)
+              mma_bf16_ts_if(leader, tmem + kO, tmem + kS + 8 * k, sdesc(vd + k * 128, v_hi),
+                             idesc_bf16(128, D, 0, 1), k > 0 ? 1u : x >= 2);
+          } else {
+#pragma unroll 1
+            for (int k = 4 * h; k < 4 * h + 4; ++k)
+              if (steps >> k & 1)
+                mma_bf16_ts_if(leader, tmem + kO, tmem + kS + 8 * k, sdesc(vd + k * 128, v_hi),
+                               idesc_bf16(128, D, 0, 1), (x >= 2 || (steps & ((1u << k) - 1))) ? 1u : 0u);
+          }
         }
-        phases ^= 1u << st;
-        if (live && x + 2 < jobs) live = issue_s(x + 2);
-      }
-      if (live && jobs == 1) {  // the second stream had nothing: its barrier keeps step
-        if (elect_one()) mma_commit(&o_full[1]);
-        __syncwarp();
-      }
-      loads += 2 * nt;
+        p_phase[st] ^= 1;
+        if (!dual || st) mma_commit_if(leader, &kv_empty[vs]);
+        if (x + 2 < jobs) return issue_s(stream);
+        mma_commit_if(leader, &o_full[st]);
+        return true;
+      };
+      using S0 = std::integral_constant<int, 0>;
+      using S1 = std::integral_constant<int, 1>;
+      live = issue_s(S0{}) && (jobs < 2 || issue_s(S1{}));
+      // the outputs of the segment before must be out of TMEM before the first PV
+      if (live && n > 0) live = wait(o_free, (uint32_t)((n - 1) & 1));
+#pragma unroll 1
+      for (int x = 0; x < jobs && live; x += 2) live = job(S0{}, x) && (x + 1 >= jobs || job(S1{}, x + 1));
+      // a single tile: the second stream had nothing, its barrier keeps step
+      if (live && jobs == 1) mma_commit_if(leader, &o_full[1]);
       release_segment(n);
     }
     // every MMA this warp issued has completed before TMEM is freed
-    if (elect_one()) mma_commit(mma_fin);
     __syncwarp();
+    mma_commit_if(leader, mma_fin);
     mbar_wait(mma_fin, 0);
   } else if (warp > kMmaWarp) {
     regs_decrease<kOtherRegs>();
@@ -634,6 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t scol = lane_base + kTmemS + st * 128;
     const float c = a.scale_log2;  // > 0: max of raw logits * c = max of scaled logits
     int jobs_seen = 0;             // tiles of this stream so far: the phase of its S barrier
+#pragma unroll 1
     for (int n = 0;; ++n) {
       const Segment* sp = next_segment(n);
       if (sp == nullptr) break;
@@ -645,13 +694,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int node = mine ? (s.row0 + row) / a.G : 0;
       const int64_t orow = (int64_t)(s.r0 + node) * a.H + s.hk * a.G + (mine ? (s.row0 + row) % a.G : 0);
       uint64_t mask = 0;
-      int64_t lo = 0;
+      int lo = 0;
       if (mine) {
         mask = a.mask[s.r0 + node] & (s.n < 64 ? (1ull << s.n) - 1 : ~0ull);
-        if (a.W >= 0) {
-          lo = a.pos[s.r0 + node] - a.W + 1;
-          lo = lo < 0 ? 0 : lo > s.L ? s.L : lo;
-        }
+        if (a.W >= 0) lo = window_start(a.pos[s.r0 + node], a.W, s.L);
       }
       // this warp's query rows into the stream's row tile (128-byte swizzle).  The products
       // that read the rows before are complete: this warp has seen the last PV (o_full) of
@@ -687,8 +733,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_run = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       bool live = true;
+#pragma unroll 1
       for (int x = st; x < jobs; x += 2) {
-        const int64_t base = (int64_t)(s.t0 + (dual ? x >> 1 : x)) * kTile;
+        const int base = (s.t0 + (dual ? x >> 1 : x)) * kTile;
         if (!wait(&s_full[st], (uint32_t)(jobs_seen++ & 1))) {
           live = false;
           break;
@@ -722,7 +769,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
 #pragma unroll
-            for (int e = 64 * h; e < 64 * h + 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
+            for (int e = 64 * h; e < 64 * h + 64; e += 2)
+              mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
           }
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
           const bool raise = mt > m_run + kRescaleSlack || (m_run == -INFINITY && mt > -INFINITY);
@@ -744,30 +792,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           m_run = m_new;
           // p = 2^(s c - m); the sums take the unrounded weights, the product with V
-          // their bf16 rounding (the tensor pipe's operand type).  Of every eight weights
-          // of an unmasked tile kPolyPairs pairs go to the fma pipe, the rest to the SFU.
+          // their bf16 rounding (the tensor pipe's operand type)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t pk[32];
-            if (all) {
 #pragma unroll
-              for (int e = 0; e < 64; e += 2) {
-                float2 z = fma2(make_float2(__uint_as_float(v[64 * h + e]), __uint_as_float(v[64 * h + e + 1])),
-                                make_float2(c, c), make_float2(-m_use, -m_use));
-                if ((e & 7) >= 8 - 2 * kPolyPairs) z = poly_exp2(z);
-                else z.x = fast_exp2(z.x), z.y = fast_exp2(z.y);
-                l2 = add2(l2, z);
-                pk[e / 2] = pack_bf16x2(z.x, z.y);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 64; e += 2) {
-                float2 z = fma2(make_float2(__uint_as_float(v[64 * h + e]), __uint_as_float(v[64 * h + e + 1])),
-                                make_float2(c, c), make_float2(-m_use, -m_use));
-                z.x = fast_exp2(z.x), z.y = fast_exp2(z.y);
-                l2 = add2(l2, z);
-                pk[e / 2] = pack_bf16x2(z.x, z.y);
-              }
+            for (int e = 0; e < 64; e += 2) {
+              float2 z = fma2(make_float2(__uint_as_float(v[64 * h + e]), __uint_as_float(v[64 * h + e + 1])), both(c),
+                              both(-m_use));
+              z.x = fast_exp2(z.x), z.y = fast_exp2(z.y);
+              l2 = add2(l2, z);
+              pk[e / 2] = pack_bf16x2(z.x, z.y);
             }
             tmem_st32p(scol + 32 * h, pk);
             if (h == 0) {
@@ -895,39 +930,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   the sequence, key head, first row of the item); parts 2, 3, .. are the first
 //   slots of CTAs c+1, c+2, ..
 // O = sum_i 2^(lse_i - lse) O_i with lse = log2 sum_i 2^lse_i, in the parts' order.
-// A warp takes a row; when there are fewer rows than blocks, the eight warps of a
-// block share the parts of one row.
-constexpr int kMaxCtas = 1024;
+// Latency bound: a block finds the rows of all items from one read of the records;
+// a warp takes a row, its lanes the parts' log-sum-exps at once, then eight parts'
+// outputs in flight.  With fewer rows than blocks the eight warps of a block share
+// the parts of one row.
+constexpr int kMaxCtas = 256;
 
 template <int D>
-__global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ TreeArgs a, int ctas) {
+__global__ void __launch_bounds__(kMaxCtas) tree_combine_kernel(const __grid_constant__ TreeArgs a, int ctas) {
+  constexpr int kWarps = kMaxCtas / 32;
+  constexpr int C = D / 32;  // channels of a lane
   __shared__ int s_rows[kMaxCtas + 1];  // rows before CTA c's item
-  __shared__ float s_o[8][D];
-  __shared__ float s_l[8];
+  __shared__ int s_warp[kWarps];
+  __shared__ float s_o[kWarps][D];
+  __shared__ float s_l[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();  // the partial results come from the attention kernel before
-  if (warp == 0) {
-    int sum = 0;
-    for (int base = 0; base < ctas; base += 32) {
-      const int4 e = base + lane < ctas ? a.split[2 * (base + lane)] : make_int4(0, 0, 0, 0);
-      const int mine = e.z > 0 ? e.x : 0;
-      int up = mine;
+  {
+    const int c = threadIdx.x;
+    const int4 e = c < ctas ? a.split[2 * c] : make_int4(0, 0, 0, 0);
+    const int rows = e.z > 0 ? e.x : 0;
+    int up = rows;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, up, o);
-        if (lane >= o) up += y;
-      }
-      if (base + lane < ctas) s_rows[base + lane] = sum + up - mine;
-      sum += __shfl_sync(0xffffffffu, up, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += y;
     }
-    if (lane == 0) s_rows[ctas] = sum;
+    if (lane == 31) s_warp[warp] = up;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) up += s_warp[w];
+    s_rows[c] = up - rows;
+    if (c == kMaxCtas - 1) s_rows[kMaxCtas] = up;
+    __syncthreads();
   }
-  __syncthreads();
-  const int rows = s_rows[ctas];
+  const int rows = s_rows[kMaxCtas];
   const bool shared = rows <= (int)gridDim.x;  // a block per row
-  const int step = shared ? gridDim.x : gridDim.x * 8;
-  for (int i = shared ? blockIdx.x : blockIdx.x * 8 + warp; i < rows; i += step) {
-    int c0 = 0, c1 = ctas;  // the last c with s_rows[c] <= i has rows
+  const int step = shared ? gridDim.x : gridDim.x * kWarps;
+  for (int i = shared ? blockIdx.x : blockIdx.x * kWarps + warp; i < rows; i += step) {
+    int c0 = 0, c1 = kMaxCtas;  // the last c with s_rows[c] <= i has rows
     while (c1 - c0 > 1) {
       const int mid = (c0 + c1) / 2;
       if (s_rows[mid] <= i) c0 = mid;
@@ -936,35 +976,46 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
     const int4 e = a.split[2 * c0], w = a.split[2 * c0 + 1];
     const int row = i - s_rows[c0];
     const int parts = e.z;
-    auto slot = [&](int p) { return p == 0 ? e.y : 2 * (c0 + p); };
+    auto at = [&](int p) { return (int64_t)(p == 0 ? e.y : 2 * (c0 + p)) * a.part_rows + row; };
     // the largest lse of all parts, then the weighted sums of this warp's
-    float m = -INFINITY;
-    for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.part_lse[(int64_t)slot(p) * a.part_rows + row]);
+    float first = -INFINITY;  // lane p: lse of part p
+    if (lane < parts) first = a.part_lse[at(lane)];
+    float m = first;
+    for (int p = 32 + lane; p < parts; p += 32) m = fmaxf(m, a.part_lse[at(p)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    constexpr int C = D / 32;
     float acc[C] = {};
     float l = 0.f;
     if (m > -INFINITY) {
-#pragma unroll 8
-      for (int p = shared ? warp : 0; p < parts; p += shared ? 8 : 1) {
-        const int64_t at = (int64_t)slot(p) * a.part_rows + row;
-        const float wt = exp2f(a.part_lse[at] - m);
-        l += wt;
+      const int stride = shared ? kWarps : 1;
+      for (int p0 = shared ? warp : 0; p0 < parts; p0 += 8 * stride) {
+        float o[8][C], wt[8];
 #pragma unroll
-        for (int j = 0; j < C; ++j) acc[j] = fmaf(wt, a.part_o[at * D + 32 * j + lane], acc[j]);
+        for (int j = 0; j < 8; ++j) {
+          const int p = p0 + j * stride;
+          const float ls = p < 32 ? __shfl_sync(0xffffffffu, first, p & 31) : p < parts ? a.part_lse[at(p)] : -INFINITY;
+          wt[j] = p < parts ? fast_exp2(ls - m) : 0.f;
+#pragma unroll
+          for (int k = 0; k < C; ++k) o[j][k] = wt[j] > 0.f ? a.part_o[at(p) * D + 32 * k + lane] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          l += wt[j];
+#pragma unroll
+          for (int k = 0; k < C; ++k) acc[k] = fmaf(wt[j], o[j][k], acc[k]);
+        }
       }
     }
     if (shared) {
 #pragma unroll
-      for (int j = 0; j < C; ++j) s_o[warp][32 * j + lane] = acc[j];
+      for (int k = 0; k < C; ++k) s_o[warp][32 * k + lane] = acc[k];
       if (lane == 0) s_l[warp] = l;
       __syncthreads();
       if (warp == 0) {
-        for (int p = 1; p < 8; ++p) {
+        for (int p = 1; p < kWarps; ++p) {
           l += s_l[p];
 #pragma unroll
-          for (int j = 0; j < C; ++j) acc[j] += s_o[p][32 * j + lane];
+          for (int k = 0; k < C; ++k) acc[k] += s_o[p][32 * k + lane];
         }
       }
       __syncthreads();
@@ -974,10 +1025,10 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
     const int64_t orow = (int64_t)(w.x + nh / a.G) * a.H + w.y * a.G + nh % a.G;
     const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int64_t at = orow * D + 32 * j + lane;
-      if (a.o_f32) static_cast<float*>(a.O)[at] = acc[j] * inv;
-      else static_cast<__nv_bfloat16*>(a.O)[at] = __float2bfloat16(acc[j] * inv);
+    for (int k = 0; k < C; ++k) {
+      const int64_t to = orow * D + 32 * k + lane;
+      if (a.o_f32) static_cast<float*>(a.O)[to] = acc[k] * inv;
+      else static_cast<__nv_bfloat16*>(a.O)[to] = __float2bfloat16(acc[k] * inv);
     }
     if (a.lse && lane == 0) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
@@ -1022,7 +1073,7 @@ cudaError_t launch_tree(const TreeArgs& a, const TreeMaps& maps, int ctas, cudaS
   if (e == cudaSuccess)
     e = launch_kernel(tree_attn_kernel<D>, dim3(ctas), dim3(kThreads), smem, stream, false, a, maps);
   if (e == cudaSuccess && ctas > 1)
-    e = launch_kernel(tree_combine_kernel<D>, dim3(4 * sm_count()), dim3(256), 0, stream, true, a, ctas);
+    e = launch_kernel(tree_combine_kernel<D>, dim3(4 * sm_count()), dim3(kMaxCtas), 0, stream, true, a, ctas);
   return e;
 }
 
