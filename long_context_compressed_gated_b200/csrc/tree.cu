@@ -9,9 +9,9 @@
 // Work.  The rows of one (sequence, key head) are its nodes times the G = H/Hk
 // query heads that share the key head, 128 to a tensor tile (TMEM lane = row).
 // Up to 256 rows make one item, which walks the keys of its sequence in tiles of
-// 128 from the first one that any row sees.  All items' key tiles, those of an item
-// of two row tiles counted twice, form one line, cut into equal shares, one per CTA
-// (one CTA per SM, persistent): lengths may be as ragged as they like.  A share that covers an item only in part writes an
+// 128 from the first one that any row sees.  All items' key tiles, each as long as it
+// takes, form one line, cut into equal shares, one per CTA (one CTA per SM,
+// persistent): lengths may be as ragged as they like.  A share that covers an item only in part writes an
 // fp32 partial (O, lse); tree_combine_kernel merges those.  Lengths are read on
 // the device, so the cut follows them in a captured graph.
 //
@@ -66,7 +66,11 @@ constexpr int kThreads = 384;       // three warpgroups (the last two warps idle
 // row of S, take 208 and the third group keeps 88 (2 * 208 + 88 = 3 * 168).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kMaxNodes = 64;       // bits of a mask
-constexpr int kMinShare = 8;        // positions of that line a CTA takes at least
+// Lengths on the line of all items' key tiles, in thirds of the time of a key tile of a
+// single row tile (1.26 us of memory traffic; a pair of row tiles takes 2.07 us): a tile
+// of a single row tile, of a pair, and what starting an item costs beside them.
+constexpr int kSingleCost = 3, kPairCost = 5, kItemCost = 12;
+constexpr int kMinShare = kItemCost + 8 * kSingleCost;  // a CTA's share at least
 constexpr float kRescaleSlack = 8.0f;  // raise the running max only when it grows by > 2^8
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -101,7 +105,12 @@ struct Seq {
   int tile0;        // first key tile
   int tiles;        // key tiles (one at least: an item without keys still writes its rows)
   int units;        // row tiles per key head: ceil(n * G / 128)
-  __device__ int64_t total(int Hk) const { return (int64_t)tiles * units * Hk; }
+  __device__ int64_t pair() const { return kItemCost + (int64_t)kPairCost * tiles; }  // an item of two row tiles
+  // length of one key head: its pairs, then perhaps an item of a single row tile
+  __device__ int64_t head() const {
+    return (units >> 1) * pair() + (units & 1) * (kItemCost + (int64_t)kSingleCost * tiles);
+  }
+  __device__ int64_t total(int Hk) const { return tiles > 0 ? head() * Hk : 0; }
 };
 
 // 2^x with the SFU (ex2.approx, ~2 ulp; -inf -> +0).
@@ -109,6 +118,10 @@ __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -410,23 +423,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         q = sequence(++b);
       }
       if (q.tiles == 0) break;
-      // the item that holds position g: a key head's items of two row tiles, then perhaps
-      // one of a single; every key tile of an item is as long as its row tiles
-      const int64_t head = (int64_t)q.tiles * q.units;  // positions of one key head
+      // the item that holds position g
+      const int64_t head = q.head(), pair = q.pair();
       Segment s;
       s.valid = 1;
       s.r0 = q.r0;
       s.n = q.n;
       s.hk = (int)div64(g - at, head);
-      const int set = (int)div64(g - at - s.hk * head, 2 * q.tiles);
+      const int set = (int)div64(g - at - s.hk * head, pair);
       s.row0 = set * kItemRows;
       const int left = q.n * a.G - s.row0;
       s.rows = left < kItemRows ? left : kItemRows;
-      const int wide = s.rows > kTile ? 2 : 1;
-      const int64_t i0 = at + s.hk * head + (int64_t)set * 2 * q.tiles, i1 = i0 + (int64_t)wide * q.tiles;
+      const int wide = s.rows > kTile ? kPairCost : kSingleCost;
+      const int64_t i0 = at + s.hk * head + set * pair, i1 = i0 + kItemCost + (int64_t)wide * q.tiles;
       const int64_t end = i1 < last ? i1 : last;
-      // a key tile goes to the share that holds its first position
-      const int t0 = (int)((g - i0 + wide - 1) >> (wide - 1)), t1 = (int)((end - i0 + wide - 1) >> (wide - 1));
+      // a key tile goes to the share that holds its first position; the item's own cost comes first
+      auto tile_from = [&](int64_t pos) {
+        const int64_t d = pos - i0 - kItemCost;
+        return d <= 0 ? 0 : ((int)d + wide - 1) / wide;
+      };
+      const int t0 = tile_from(g), t1 = tile_from(end);
       g = end;
       if (t0 == t1) continue;
       s.t0 = q.tile0 + t0;
@@ -435,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       s.lo = q.lo;
       s.slot = t0 == 0 && t1 == q.tiles ? -1 : (int)(2 * c) + (n == 0 ? 0 : 1);
       if (t0 == 0 && t1 < q.tiles) {  // the item goes on in the next CTAs: tell the combine
-        const int64_t tail = i0 + (int64_t)wide * (q.tiles - 1);  // its last tile
+        const int64_t tail = i0 + kItemCost + (int64_t)wide * (q.tiles - 1);  // its last tile
         int64_t cl = div64(tail * ctas, total);
         while (div64((cl + 1) * total, ctas) <= tail) ++cl;
         split = make_int4(s.rows, s.slot, (int)(cl - c + 1), 0);
@@ -449,6 +465,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         *reinterpret_cast<Segment*>(s_seg + (n & 1) * 128) = s;
         mbar_arrive(&seg_full[n & 1]);
+      }
+      // the rows that the softmax warps will read when they get to this segment (n > 0: while
+      // the one before runs), into L2 now: behind the ring's loads they take up to 13 us
+      if (n > 0) {
+        for (int i = lane; i < s.rows; i += 32) {
+          const int row = s.row0 + i;
+          const int64_t orow = (int64_t)(s.r0 + row / a.G) * a.H + s.hk * a.G + row % a.G;
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) prefetch_l2(a.q + orow * D + 64 * h);
+        }
       }
       // K and V tiles
       const bool dual = s.rows > kTile;
@@ -708,22 +734,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ch = lane % LPR;
         const uint32_t dst = smem_u32(s_q) + (uint32_t)(st * L::kTileBytes + (ch >> 3) * kHalfBytes);
         const int64_t off = mine ? orow * D : -1;
+        uint4 v[LPR];
 #pragma unroll
-        for (int i0 = 0; i0 < 32; i0 += 8 * RPW) {
-          uint4 v[8];
+        for (int i = 0; i < LPR; ++i) {
+          const int64_t from = __shfl_sync(0xffffffffu, off, i * RPW + lane / LPR);
+          v[i] = from >= 0 ? *reinterpret_cast<const uint4*>(a.q + from + 8 * ch) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int64_t from = __shfl_sync(0xffffffffu, off, i0 + i * RPW + lane / LPR);
-            v[i] = from >= 0 ? *reinterpret_cast<const uint4*>(a.q + from + 8 * ch) : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = (warp & 3) * 32 + i0 + i * RPW + lane / LPR;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + r * 128 +
-                                                                          (uint32_t)(((ch & 7) ^ (r & 7)) << 4)),
-                         "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
-                         : "memory");
-          }
+        for (int i = 0; i < LPR; ++i) {
+          const int r = (warp & 3) * 32 + i * RPW + lane / LPR;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + r * 128 +
+                                                                        (uint32_t)(((ch & 7) ^ (r & 7)) << 4)),
+                       "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
+                       : "memory");
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -1056,7 +1079,7 @@ int tree_ctas(int B, int64_t R, int H, int Hk, int page, int max_pages) {
   const int64_t seqs = B < R ? B : R;  // with a node
   const int64_t items = Hk * (seqs + R * (H / Hk) / kTile);  // row tiles
   const int64_t tiles = ceil_div((int64_t)max_pages * page, kTile) + (nodes > 0 ? 1 : 0);
-  const int64_t most = items * tiles / kMinShare;
+  const int64_t most = items * (kItemCost + tiles * kSingleCost) / kMinShare;
   return (int)(most < 1 ? 1 : most < sms ? most : sms);
 }
 
