@@ -17,8 +17,8 @@
 //
 // One CTA:
 //   warps 0..3, 4..7  two softmax streams, one thread per row;
-//   warp 8            walks the share, publishes its segments, fetches K and V
-//                     pages by TMA (one box per page and 64 channels);
+//   warp 8            walks the share and publishes its segments;
+//   warps 8, 10       fetch K and V pages by TMA (one box per page and 64 channels);
 //   warp 9            TMEM and MMA issue.
 // An item of more than 128 rows gives each stream one row tile, and both use
 // every K/V tile; a smaller item gives both streams the same rows and alternate
@@ -60,16 +60,17 @@ namespace {
 constexpr int kTile = 128;          // rows of a tensor tile, keys of a key tile
 constexpr int kItemRows = 2 * kTile;
 constexpr int kSoftmaxWarps = 8;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 384;       // three warpgroups (the last two warps idle)
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kLoadWarp2 = 10;
+constexpr int kThreads = 384;       // three warpgroups (the last warp idles)
 // Registers: 384 threads launch with 168 each; the softmax groups, which hold a
 // row of S, take 208 and the third group keeps 88 (2 * 208 + 88 = 3 * 168).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kMaxNodes = 64;       // bits of a mask
-// Lengths on the line of all items' key tiles, in thirds of the time of a key tile of a
-// single row tile (1.26 us of memory traffic; a pair of row tiles takes 2.07 us): a tile
-// of a single row tile, of a pair, and what starting an item costs beside them.
-constexpr int kSingleCost = 3, kPairCost = 5, kItemCost = 12;
+// Lengths on the line of all items' key tiles, in key tiles of a single row tile (1.0 us;
+// a pair of row tiles takes 2.07 us): a tile of a single row tile, of a pair, and what
+// starting an item costs beside them (outputs written, query rows read: 3.5 us each,
+// partly hidden).
+constexpr int kSingleCost = 1, kPairCost = 2, kItemCost = 4;
 constexpr int kMinShare = kItemCost + 8 * kSingleCost;  // a CTA's share at least
 constexpr float kRescaleSlack = 8.0f;  // raise the running max only when it grows by > 2^8
 constexpr float kLn2 = 0.69314718055994531f;
@@ -199,7 +200,7 @@ __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) { return a / b; }
 // One segment of a share: part of one item.
 struct Segment {
   int valid;
-  int r0, n;          // the sequence's first row and nodes
+  int b, r0, n;       // the sequence, its first row and nodes
   int row0, rows;     // the item's first (node, head) row and its rows
   int hk;
   int t0, t1;         // its key tiles, counted from tile 0 of the sequence
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_full[i], 1);
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_free[i], kSoftmaxWarps + 1);
+      mbar_init(&seg_free[i], kSoftmaxWarps + 2);
     }
     mbar_init(mma_fin, 1);
     mbar_init(o_free, kSoftmaxWarps);
@@ -349,6 +350,79 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto release_segment = [&](int n) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&seg_free[n & 1]);
+  };
+
+  // K and V tiles of a segment, by two warps (a tile's fetch takes a warp about 0.5 us: page
+  // numbers, and some 80 cycles a box): each takes every other place of the ring.  Order of
+  // the places, the order in which the MMA warp uses the tiles: K0 V0 K1 V1 .. when both
+  // streams work on every tile, K0 K1 V0 K2 V1 .. when they alternate.
+  const int loader = warp == kLoadWarp ? 0 : 1;
+  int loads = 0;    // ring position of the segment's first tile
+  int issued = -1;  // this warp's last
+  auto load_tiles = [&](const Segment& s, int n) -> bool {
+    const bool dual = s.rows > kTile;
+    const int nt = s.t1 - s.t0, S = s.L + s.n;
+    const int box_rows = a.page_shift < 7 ? 1 << a.page_shift : kTile;
+    const int boxes = kTile / box_rows * HALVES;  // per tile, at most 16
+    const int my_row = lane / HALVES * box_rows, my_half = lane % HALVES;
+    uint8_t* const dst = s_kv + my_half * kHalfBytes + my_row * 128;
+    const int lo = s.lo, hk_row = s.hk << a.page_shift, page_mask = (1 << a.page_shift) - 1;
+    // page numbers are read ahead: lane l holds entries from + l and from + 32 + l of the
+    // sequence's table (a tile's pages lie within one run of 32: both start at multiples
+    // of 128 keys)
+    const int32_t* table = a.table + (int64_t)s.b * a.max_pages;
+    const int last_page = (S - 1) >> a.page_shift;  // (a sequence with a node has S >= 1)
+    auto entry = [&](int p) { return p <= last_page ? table[p] : -1; };
+    int from = (s.t0 * kTile) >> a.page_shift;
+    int now = entry(from + lane), next = entry(from + 32 + lane);
+    bool hold = n == 0;
+#pragma unroll 1
+    for (int i = loader; i < 2 * nt; i += 2) {
+      int t, kind;
+      if (dual) {
+        t = i >> 1, kind = loader;
+      } else if (i == 0 || i == 2 * nt - 1) {
+        t = i == 0 ? 0 : nt - 1, kind = i == 0 ? 0 : 1;
+      } else {
+        kind = loader ? 0 : 1;
+        t = kind ? i / 2 - 1 : (i + 1) / 2;
+      }
+      // at the start the query rows go first: behind a ring full of K and V they would wait
+      // for all of it
+      if (hold && i >= (dual || nt == 1 ? 1 : 2)) {
+        if (!wait(&q_full[0], 0) || (dual && !wait(&q_full[1], 0))) return false;
+        hold = false;
+      }
+      const int key0 = (s.t0 + t) * kTile, key = key0 + my_row;
+      if (key0 >> a.page_shift >= from + 32) {
+        from += 32;
+        now = next;
+        next = entry(from + 32 + lane);
+      }
+      int page = __shfl_sync(0xffffffffu, now, ((key >> a.page_shift) - from) & 31);
+      const bool need = lane < boxes && key + box_rows > lo && key < S;
+      if (need && (page < 0 || page >= a.n_pages)) {
+        report(a.status, CSA_ERR_INDEX);
+        page = a.n_pages > 0 ? (int)a.n_pages : 1;  // outside the map: zeros
+      }
+      const int count = __popc(__ballot_sync(0xffffffffu, need));
+      const int at = loads + i, sg = at % kStages;
+      if (at >= kStages && !wait(&kv_empty[sg], (uint32_t)((at / kStages - 1) & 1))) return false;
+      issued = at;
+      if (lane == 0) mbar_arrive_expect_tx(&kv_full[sg], (uint32_t)(count * box_rows * 128));
+      __syncwarp();
+      if (need)
+        tma_load_3d(dst + (size_t)sg * L::kTileBytes, kind ? &maps.v : &maps.k, &kv_full[sg], my_half * 64,
+                    hk_row + (key & page_mask), page);
+    }
+    loads += 2 * nt;
+    return true;
+  };
+  // after an abort, wait (bounded) for this warp's loads still landing in shared memory
+  auto drain = [&]() {
+    if (*s_abort && lane == 0)
+      for (int at = issued; at >= 0 && at > issued - kStages; at -= 2)
+        mbar_wait(&kv_full[at % kStages], (uint32_t)((at / kStages) & 1));
   };
 
   if (warp == kLoadWarp) {
@@ -412,8 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       q.units = __shfl_sync(0xffffffffu, mine.units, w);
       return q;
     };
-    int loads = 0;  // tiles fetched so far (ring position)
-    int n = 0;      // segments published
+    int n = 0;  // segments published
     bool live = true;
 #pragma unroll 1
     for (int64_t g = first; g < last && live;) {
@@ -427,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t head = q.head(), pair = q.pair();
       Segment s;
       s.valid = 1;
+      s.b = b;
       s.r0 = q.r0;
       s.n = q.n;
       s.hk = (int)div64(g - at, head);
@@ -476,74 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; h < HALVES; ++h) prefetch_l2(a.q + orow * D + 64 * h);
         }
       }
-      // K and V tiles
-      const bool dual = s.rows > kTile;
-      const int nt = s.t1 - s.t0;
-      const int box_rows = a.page_shift < 7 ? 1 << a.page_shift : kTile;
-      const int boxes = kTile / box_rows * HALVES;  // per tile, at most 16
-      const int my_row = lane / HALVES * box_rows, my_half = lane % HALVES;
-      // Page numbers are read ahead: lane l holds entries from + l and from + 32 + l of the
-      // sequence's table, one pair for K and one for V (which is up to two tiles behind)
-      const int32_t* table = a.table + (int64_t)b * a.max_pages;
-      const int last_page = (q.S - 1) >> a.page_shift;  // (a sequence with a node has S >= 1)
-      auto entry = [&](int p) { return p <= last_page ? table[p] : -1; };
-      const int from0 = (s.t0 * kTile) >> a.page_shift;
-      int from[2] = {from0, from0};
-      int now[2], next[2];
-      now[0] = now[1] = entry(from0 + lane);
-      next[0] = next[1] = entry(from0 + 32 + lane);
-#pragma unroll 1
-      for (int i = 0; i < 2 * nt && live; ++i) {
-        // load i of the segment: which tile of which kind
-        int t, kind;
-        if (dual) {
-          t = i >> 1, kind = i & 1;
-        } else if (i == 0 || i == 2 * nt - 1) {
-          t = i == 0 ? 0 : nt - 1, kind = i == 0 ? 0 : 1;
-        } else {
-          kind = (i & 1) ? 0 : 1;
-          t = kind ? i / 2 - 1 : (i + 1) / 2;
-        }
-        const int st = loads % kStages;
-        if (loads >= kStages && !wait(&kv_empty[st], (uint32_t)((loads / kStages - 1) & 1))) {
-          live = false;
-          break;
-        }
-        const int key = (s.t0 + t) * kTile + my_row;
-        const bool need = lane < boxes && key + box_rows > q.lo && key < q.S;
-        // (a tile's pages lie within one run of 32: both start at multiples of 128 keys)
-        int page = 0;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if (kind != k) continue;
-          if (((s.t0 + t) * kTile) >> a.page_shift >= from[k] + 32) {
-            from[k] += 32;
-            now[k] = next[k];
-            next[k] = entry(from[k] + 32 + lane);
-          }
-          page = __shfl_sync(0xffffffffu, now[k], ((key >> a.page_shift) - from[k]) & 31);
-        }
-        if (need && (page < 0 || page >= a.n_pages)) {
-          report(a.status, CSA_ERR_INDEX);
-          page = a.n_pages > 0 ? (int)a.n_pages : 1;  // outside the map: zeros
-        }
-        // at the start the query rows go first: behind a ring full of K and V they would
-        // wait for all of it
-        if (n == 0 && i == (dual || nt == 1 ? 1 : 2) &&
-            (!wait(&q_full[0], 0) || (dual && !wait(&q_full[1], 0)))) {
-          live = false;
-          break;
-        }
-        const int count = __popc(__ballot_sync(0xffffffffu, need));
-        if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], (uint32_t)(count * box_rows * 128));
-        __syncwarp();
-        if (need) {
-          const int row = (s.hk << a.page_shift) + (key & ((1 << a.page_shift) - 1));
-          tma_load_3d(s_kv + (size_t)st * L::kTileBytes + my_half * kHalfBytes + my_row * 128,
-                      kind ? &maps.v : &maps.k, &kv_full[st], my_half * 64, row, page);
-        }
-        ++loads;
-      }
+      if (!load_tiles(s, n)) break;
       ++n;
     }
     if (lane == 0) a.split[2 * c] = split;
@@ -552,10 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       reinterpret_cast<Segment*>(s_seg + (n & 1) * 128)->valid = 0;
       mbar_arrive(&seg_full[n & 1]);
     }
-    // after an abort, wait (bounded) for the loads still landing in shared memory
-    if (*s_abort && lane == 0)
-      for (int i = loads > kStages ? loads - kStages : 0; i < loads; ++i)
-        mbar_wait(&kv_full[i % kStages], (uint32_t)((i / kStages) & 1));
+    drain();
   } else if (warp == kMmaWarp) {
     regs_decrease<kOtherRegs>();
     // =========================== MMA issue
@@ -697,7 +701,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     mma_commit_if(leader, mma_fin);
     mbar_wait(mma_fin, 0);
-  } else if (warp > kMmaWarp) {
+  } else if (warp == kLoadWarp2) {
+    regs_decrease<kOtherRegs>();
+    // =========================== the other half of the K / V tiles
+#pragma unroll 1
+    for (int n = 0;; ++n) {
+      const Segment* sp = next_segment(n);
+      if (sp == nullptr || !load_tiles(*sp, n)) break;
+      release_segment(n);
+    }
+    drain();
+  } else if (warp > kLoadWarp2) {
     regs_decrease<kOtherRegs>();
   } else {
     regs_increase<kSoftmaxRegs>();
@@ -954,24 +968,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   slots of CTAs c+1, c+2, ..
 // O = sum_i 2^(lse_i - lse) O_i with lse = log2 sum_i 2^lse_i, in the parts' order.
 // Latency bound: a block finds the rows of all items from one read of the records;
-// a warp takes a row, its lanes the parts' log-sum-exps at once, then eight parts'
-// outputs in flight.  With fewer rows than blocks the eight warps of a block share
-// the parts of one row.
+// a warp takes a row and loads eight parts' log-sum-exps and outputs at once.  With
+// fewer rows than blocks the eight warps of a block share the parts of one row.
 constexpr int kMaxCtas = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kMaxCtas) tree_combine_kernel(const __grid_constant__ TreeArgs a, int ctas) {
+__global__ void __launch_bounds__(kMaxCtas, 4) tree_combine_kernel(const __grid_constant__ TreeArgs a, int ctas) {
   constexpr int kWarps = kMaxCtas / 32;
   constexpr int C = D / 32;  // channels of a lane
   __shared__ int s_rows[kMaxCtas + 1];  // rows before CTA c's item
+  __shared__ int4 s_item[kMaxCtas][2];
   __shared__ int s_warp[kWarps];
   __shared__ float s_o[kWarps][D];
-  __shared__ float s_l[kWarps];
+  __shared__ float2 s_ml[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();  // the partial results come from the attention kernel before
   {
     const int c = threadIdx.x;
-    const int4 e = c < ctas ? a.split[2 * c] : make_int4(0, 0, 0, 0);
+    int4 e = make_int4(0, 0, 0, 0), w = e;
+    if (c < ctas) e = a.split[2 * c], w = a.split[2 * c + 1];
     const int rows = e.z > 0 ? e.x : 0;
     int up = rows;
 #pragma unroll
@@ -981,8 +996,9 @@ __global__ void __launch_bounds__(kMaxCtas) tree_combine_kernel(const __grid_con
     }
     if (lane == 31) s_warp[warp] = up;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) up += s_warp[w];
+    for (int i = 0; i < warp; ++i) up += s_warp[i];
     s_rows[c] = up - rows;
+    s_item[c][0] = e, s_item[c][1] = w;
     if (c == kMaxCtas - 1) s_rows[kMaxCtas] = up;
     __syncthreads();
   }
@@ -996,49 +1012,56 @@ __global__ void __launch_bounds__(kMaxCtas) tree_combine_kernel(const __grid_con
       if (s_rows[mid] <= i) c0 = mid;
       else c1 = mid;
     }
-    const int4 e = a.split[2 * c0], w = a.split[2 * c0 + 1];
+    const int4 e = s_item[c0][0], w = s_item[c0][1];
     const int row = i - s_rows[c0];
     const int parts = e.z;
-    auto at = [&](int p) { return (int64_t)(p == 0 ? e.y : 2 * (c0 + p)) * a.part_rows + row; };
-    // the largest lse of all parts, then the weighted sums of this warp's
-    float first = -INFINITY;  // lane p: lse of part p
-    if (lane < parts) first = a.part_lse[at(lane)];
-    float m = first;
-    for (int p = 32 + lane; p < parts; p += 32) m = fmaxf(m, a.part_lse[at(p)]);
+    // running maximum m of the log-sum-exps, sum l of the weights 2^(lse - m), weighted outputs
+    float m = -INFINITY, l = 0.f, acc[C] = {};
+    const int stride = shared ? kWarps : 1;
+    for (int p0 = shared ? warp : 0; p0 < parts; p0 += 8 * stride) {
+      float ls[8], o[8][C];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float acc[C] = {};
-    float l = 0.f;
-    if (m > -INFINITY) {
-      const int stride = shared ? kWarps : 1;
-      for (int p0 = shared ? warp : 0; p0 < parts; p0 += 8 * stride) {
-        float o[8][C], wt[8];
+      for (int j = 0; j < 8; ++j) {
+        const int p = p0 + j * stride;
+        const int64_t at = (int64_t)(p == 0 ? e.y : 2 * (c0 + p)) * a.part_rows + row;
+        ls[j] = p < parts ? a.part_lse[at] : -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int p = p0 + j * stride;
-          const float ls = p < 32 ? __shfl_sync(0xffffffffu, first, p & 31) : p < parts ? a.part_lse[at(p)] : -INFINITY;
-          wt[j] = p < parts ? fast_exp2(ls - m) : 0.f;
+        for (int k = 0; k < C; ++k) o[j][k] = p < parts ? a.part_o[at * D + 32 * k + lane] : 0.f;
+      }
+      float mn = m;
 #pragma unroll
-          for (int k = 0; k < C; ++k) o[j][k] = wt[j] > 0.f ? a.part_o[at(p) * D + 32 * k + lane] : 0.f;
-        }
+      for (int j = 0; j < 8; ++j) mn = fmaxf(mn, ls[j]);
+      if (mn == -INFINITY) continue;  // no part has a key yet
+      const float f = fast_exp2(m - mn);
+      m = mn, l *= f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          l += wt[j];
+      for (int k = 0; k < C; ++k) acc[k] *= f;
 #pragma unroll
-          for (int k = 0; k < C; ++k) acc[k] = fmaf(wt[j], o[j][k], acc[k]);
-        }
+      for (int j = 0; j < 8; ++j) {
+        const float wt = fast_exp2(ls[j] - m);
+        l += wt;
+#pragma unroll
+        for (int k = 0; k < C; ++k) acc[k] = fmaf(wt, o[j][k], acc[k]);
       }
     }
     if (shared) {
 #pragma unroll
       for (int k = 0; k < C; ++k) s_o[warp][32 * k + lane] = acc[k];
-      if (lane == 0) s_l[warp] = l;
+      if (lane == 0) s_ml[warp] = make_float2(m, l);
       __syncthreads();
       if (warp == 0) {
-        for (int p = 1; p < kWarps; ++p) {
-          l += s_l[p];
+        float mn = m;
+        for (int p = 1; p < kWarps; ++p) mn = fmaxf(mn, s_ml[p].x);
+        const float m_use = mn == -INFINITY ? 0.f : mn;
+        const float f = fast_exp2(m - m_use);
+        m = mn, l *= f;
 #pragma unroll
-          for (int k = 0; k < C; ++k) acc[k] += s_o[p][32 * k + lane];
+        for (int k = 0; k < C; ++k) acc[k] *= f;
+        for (int p = 1; p < kWarps; ++p) {
+          const float wt = fast_exp2(s_ml[p].x - m_use);
+          l += wt * s_ml[p].y;
+#pragma unroll
+          for (int k = 0; k < C; ++k) acc[k] = fmaf(wt, s_o[p][32 * k + lane], acc[k]);
         }
       }
       __syncthreads();
@@ -1095,8 +1118,11 @@ cudaError_t launch_tree(const TreeArgs& a, const TreeMaps& maps, int ctas, cudaS
   cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess)
     e = launch_kernel(tree_attn_kernel<D>, dim3(ctas), dim3(kThreads), smem, stream, false, a, maps);
+  // at most a warp per row of the call, and what the GPU holds at once
+  const int64_t rows = ceil_div(a.R * a.H, kMaxCtas / 32), most = 4 * (int64_t)sm_count();
+  const unsigned grid = (unsigned)(rows < most ? rows : most);
   if (e == cudaSuccess && ctas > 1)
-    e = launch_kernel(tree_combine_kernel<D>, dim3(4 * sm_count()), dim3(kMaxCtas), 0, stream, true, a, ctas);
+    e = launch_kernel(tree_combine_kernel<D>, dim3(grid), dim3(kMaxCtas), 0, stream, true, a, ctas);
   return e;
 }
 
