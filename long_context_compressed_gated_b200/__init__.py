@@ -113,9 +113,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# torch's own accessor of the current stream's handle by device number, where it has one: the
+# public one builds a Stream object, over a microsecond a call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream():
-    # (with the device's number torch skips looking it up, several microseconds a call)
-    return torch.cuda.current_stream(torch.cuda.current_device()).cuda_stream
+    dev = torch.cuda.current_device()
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _dev(t, dtype, name, ndim=None):
@@ -462,8 +467,29 @@ def _here(*tensors):
     """Every given tensor is on the current CUDA device."""
     cur = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.device.index != cur:
+        if t is not None and t.get_device() != cur:
             raise ValueError("tensors must be on the current CUDA device (cuda:%d), got %s" % (cur, t.device))
+
+
+def _like(x, dtype):
+    """A dense tensor of x's shape on its device."""
+    return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
+
+
+def _given(t, dtype, shape, name):
+    """An output that the caller supplies."""
+    _dev(t, dtype, name)
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return t
+
+
+def _scratch(workspace, device, bytes_needed):
+    """The caller's workspace (its size is checked by the library), or a new one of
+    bytes_needed() bytes with a clear status word."""
+    if workspace is not None:
+        return _dev(workspace, torch.uint8, "workspace")
+    return _workspace(bytes_needed(), device)
 
 
 def _rows(t, dtypes, name):
@@ -471,12 +497,12 @@ def _rows(t, dtypes, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dtype not in dtypes:
-        raise TypeError("%s must be one of %s, got %s" % (name, dtypes, t.dtype))
+        raise TypeError("%s must be one of %s, got %s" % (name, tuple(dtypes), t.dtype))
     if t.dim() != 3:
         raise ValueError("%s must have 3 dims, got %d" % (name, t.dim()))
     T, heads, d = t.shape
     rs, hs, cs = t.stride()
-    if T and heads and ((d > 1 and cs != 1) or (heads > 1 and hs != d)):
+    if (cs != 1 and d > 1 or hs != d and heads > 1) and t.numel():
         raise ValueError("%s must have dense [heads, d] rows" % name)
     return (rs if T > 1 else heads * d), heads
 
@@ -531,11 +557,14 @@ def csa_qk_norm_rope(q, k, inv_freq, wq=None, wk=None, eps=1e-6, pos=None, t0=0,
     ot = x.dtype if out_dtype is None else out_dtype
     _weight(wq, d, "wq"), _weight(wk, d, "wk"), _vector(pos, T, torch.int64, "pos")
     fp, rot = _freq(inv_freq)
-    yq = _out(yq, x, (T, H, d), ot, "yq") if q is not None else None
-    yk = _out(yk, x, (T, Hk, d), ot, "yk") if k is not None else None
-    for y, s, n in ((yq, q, "yq"), (yk, k, "yk")):
-        if y is not None and y.shape != s.shape:
-            raise ValueError("%s must have shape %s" % (n, tuple(s.shape)))
+    if ot not in _ODTYPE:
+        raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+    if q is not None:
+        yq = _like(q, ot) if yq is None else _given(yq, ot, q.shape, "yq")
+    if k is not None:
+        yk = _like(k, ot) if yk is None else _given(yk, ot, k.shape, "yk")
+    if q is None and yq is not None or k is None and yk is not None:
+        raise ValueError("an output without its input")
     _here(q, k, wq, wk, pos, yq, yk)
     _check(lib().csa_qk_norm_rope(_ptr(q), qs, _ptr(k), ks, _ptr(wq), _ptr(wk), eps, _ptr(pos), t0, fp, rot_start, rot,
                                   rot_style, T, H, Hk, d, _ODTYPE[x.dtype], _ptr(yq), _ptr(yk), _ODTYPE[ot],
@@ -564,19 +593,19 @@ def csa_qk_norm_rope_backward(q, k, dyq, dyk, inv_freq, wq=None, wk=None, eps=1e
             sides.append((None, None, 0, None))
             continue
         _dev(dy, yt, "dy" + n, 3)
-        dx = torch.empty(s.shape, dtype=s.dtype, device=s.device) if dx is None else dx
+        dx = _like(s, s.dtype) if dx is None else dx
         dxs, _ = _rows(dx, (s.dtype,), "d" + n)
         if dy.shape != s.shape or dx.shape != s.shape:
             raise ValueError("dy%s and d%s must have shape %s" % (n, n, tuple(s.shape)))
         if w is not None:
-            dw = torch.empty(d, dtype=torch.float32, device=s.device) if dw is None else _weight(dw, d, "dw" + n)
+            dw = torch.empty_like(w) if dw is None else _weight(dw, d, "dw" + n)
         elif dw is not None:
             raise ValueError("dw%s without w%s" % (n, n))
         sides.append((dy, dx, dxs, dw))
     (dyq, dq, dqs, dwq), (dyk, dk, dks, dwk) = sides
     L = lib()
     _here(q, k, wq, wk, pos, dyq, dyk, dq, dk, dwq, dwk, workspace)
-    ws = _workspace(L.csa_qk_norm_rope_backward_workspace_bytes(T, H, Hk, d), x.device, workspace)
+    ws = _scratch(workspace, x.device, lambda: L.csa_qk_norm_rope_backward_workspace_bytes(T, H, Hk, d))
     _check(L.csa_qk_norm_rope_backward(_ptr(q), qs, _ptr(k), ks, _ptr(wq) if H else None, _ptr(wk) if Hk else None,
                                        eps, _ptr(pos), t0, fp, rot_start, rot, rot_style, _ptr(dyq), _ptr(dyk), T, H,
                                        Hk, d, _ODTYPE[x.dtype], _ODTYPE[yt], _ptr(dq), dqs, _ptr(dk), dks, _ptr(dwq),
@@ -611,7 +640,7 @@ def csa_paged_append(k, v, Kpages, Vpages, block_table, seq, pos, inv_freq, slot
     _weight(wk, d, "wk")
     fp, rot = _freq(inv_freq)
     _here(k, v, Kpages, Vpages, block_table, seq, pos, slot, wk, workspace)
-    ws = _workspace(256, k.device, workspace)
+    ws = _scratch(workspace, k.device, lambda: 256)
     _check(lib().csa_paged_append(_ptr(k), ks, _ptr(v), vs, _ptr(wk), eps, _ptr(pos), _ptr(slot), _ptr(seq), fp,
                                   rot_start, rot, rot_style, _ptr(block_table), T, Hk, d, block_table.shape[0],
                                   block_table.shape[1], n_pages, page, _ptr(Kpages), _ptr(Vpages), _ptr(ws),
@@ -634,18 +663,16 @@ def csa_tree_attn(q, Kpages, Vpages, block_table, seq_lens, q_start, mask, scale
     B, max_pages = block_table.shape
     _vector(seq_lens, B, torch.int32, "seq_lens"), _vector(q_start, B + 1, torch.int32, "q_start")
     _vector(mask, R, torch.int64, "mask"), _vector(pos, R, torch.int64, "pos")
-    O = _out(O, q, q.shape, out_dtype)
-    if O.shape != q.shape:
-        raise ValueError("O must have shape %s" % (tuple(q.shape),))
+    if out_dtype not in _ODTYPE:
+        raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+    O = _like(q, out_dtype) if O is None else _given(O, out_dtype, q.shape, "O")
     if lse is not None:
-        _dev(lse, torch.float32, "lse", 2)
-        if lse.shape != (R, H):
-            raise ValueError("lse must have shape (%d, %d)" % (R, H))
+        _given(lse, torch.float32, (R, H), "lse")
     elif want_lse:
         lse = torch.empty(R, H, dtype=torch.float32, device=q.device)
     L = lib()
     _here(q, Kpages, Vpages, block_table, seq_lens, q_start, mask, pos, O, lse, workspace)
-    ws = _workspace(L.csa_tree_attn_workspace_bytes(B, R, H, Hk, d, page, max_pages), q.device, workspace)
+    ws = _scratch(workspace, q.device, lambda: L.csa_tree_attn_workspace_bytes(B, R, H, Hk, d, page, max_pages))
     _check(L.csa_tree_attn(_ptr(q), _ptr(Kpages), _ptr(Vpages), _ptr(block_table), _ptr(seq_lens), _ptr(q_start),
                            _ptr(mask), _ptr(pos), R, B, H, Hk, d, page, n_pages, max_pages, W, scale, _ptr(O),
                            _ODTYPE[out_dtype], _ptr(lse), _ptr(ws), ws.numel(), _stream()), "csa_tree_attn")

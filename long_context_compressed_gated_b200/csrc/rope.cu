@@ -19,22 +19,36 @@
 namespace csa {
 
 bool rope_params(const double* inv_freq, int rot, RopeParams& p) {
-  constexpr long double kTurn = 6.283185307179586476925286766559L;
+  constexpr long double kTurns = 0.15915494309189533576888376337251436L;  // 1 / 2 pi
+  constexpr long double k64 = 18446744073709551616.0L;                    // 2^64
   for (int i = 0; i < rot / 2; ++i) {
     if (!std::isfinite(inv_freq[i])) return false;
-    const long double t = (long double)inv_freq[i] / kTurn;
-    const long double frac = t - std::floor(t);  // [0, 1)
-    const long double f = std::floor(frac * 18446744073709551616.0L + 0.5L);
-    p.turn[i] = f >= 18446744073709551616.0L ? 0 : (uint64_t)f;
+    long double t = (long double)inv_freq[i] * kTurns;
+    if (!(t < 0.5L && t > -0.5L)) t -= std::floor(t + 0.5L);  // whole turns a position change nothing
+    // now in [-1/2, 1/2): a signed 64-bit fraction, whose wrapped value is the phase
+    const long double f = t * k64;
+    p.turn[i] = f >= 9223372036854775808.0L ? 1ull << 63 : (uint64_t)std::llrint(f);
   }
   return true;
 }
 
+int rope_head_chunk(int64_t T, int heads, int d, int most) {
+  const int64_t groups = (int64_t)sm_count() * (384 / (d / 8));
+  int c = most;
+  while (c > 2 && T * ceil_div(heads, c) < groups) c /= 2;
+  return c < heads ? c : heads;
+}
+
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kAhead = 4;        // rows of a group loaded before the first is used
-constexpr int kHeadChunk = 16;   // heads of one token that share a set of coefficients
+constexpr int kThreads = 256;      // forward
+constexpr int kAhead = 4;          // rows of a group loaded before the first is used
+// Backward: the bytes in flight are limited by its registers.  Measured on 16384 tokens of
+// 65 heads of 128 (bf16, with the sum of dw; the bytes alone take 125 us): 151 us with five
+// blocks of 128 threads per SM, 157 with three of 256, 168 with two of 256, 175 with four
+// of 256 (one row ahead); fetching the next unit's rows into L2 ahead: 198.
+constexpr int kBwdThreads = 128, kBwdBlocks = 5, kBwdAhead = 2;
+constexpr int kHeadChunk = 16;     // most heads of one token that share a set of coefficients
 
 // Queries or keys of one call.
 struct RopeSide {
@@ -103,8 +117,9 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
 // of dw in registers, and the block adds its groups' shares in order: one partial
 // row per block, summed in order by norm_rope_dw_kernel (no atomics).
 template <int D, typename TX, typename TY, int STYLE>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
+__global__ void __launch_bounds__(kBwdThreads, kBwdBlocks)
+    norm_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int LPR = D / 8, GROUPS = kBwdThreads / LPR;
   __shared__ uint64_t s_turn[kRopeMaxPairs];
   __shared__ float s_dw[GROUPS * D];
   stage_turns(a.p, s_turn);
@@ -128,11 +143,10 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
     const TX* x = static_cast<const TX*>(sd.x) + t * sd.x_stride + (int64_t)h0 * D + 8 * rl.l;
     const TY* dy = static_cast<const TY*>(sd.dy) + (t * sd.heads + h0) * D + 8 * rl.l;
     TX* dx = static_cast<TX*>(sd.dx) + t * sd.dx_stride + (int64_t)h0 * D + 8 * rl.l;
-    constexpr int AHEAD = 2;
-    RawX rx[AHEAD];
-    RawY ry[AHEAD];
+    RawX rx[kBwdAhead];
+    RawY ry[kBwdAhead];
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u)
+    for (int u = 0; u < kBwdAhead; ++u)
       if (u < n) load8(x + u * D, rx[u]), load8(dy + u * D, ry[u]);
     float A[8], B[8];
     {
@@ -142,15 +156,15 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
       for (int j = 0; j < 8; ++j) s[j] = -s[j];  // the transpose turns back
       rope_coef<STYLE>(rl, c, s, one, one, A, B);
     }
-    for (int h = 0; h < n; h += AHEAD) {
+    for (int h = 0; h < n; h += kBwdAhead) {
 #pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
+      for (int u = 0; u < kBwdAhead; ++u) {
         if (h + u >= n) break;
         const RawX cx = rx[u];
         const RawY cy = ry[u];
-        if (h + u + AHEAD < n) {
-          load8(x + (int64_t)(h + u + AHEAD) * D, rx[u]);
-          load8(dy + (int64_t)(h + u + AHEAD) * D, ry[u]);
+        if (h + u + kBwdAhead < n) {
+          load8(x + (int64_t)(h + u + kBwdAhead) * D, rx[u]);
+          load8(dy + (int64_t)(h + u + kBwdAhead) * D, ry[u]);
         }
         float f[8], e[8], g[8];
         unpack8(cx, f);
@@ -212,22 +226,20 @@ __global__ void __launch_bounds__(8 * D) norm_rope_dw_kernel(const float* part, 
   }
 }
 
-// Thread blocks that one pass over a side takes.
-int64_t side_blocks(int64_t T, int heads, int d) {
-  return ceil_div(T * ceil_div(heads, kHeadChunk), kThreads / (d / 8));
-}
+int64_t side_units(int64_t T, int heads, int d) { return T * ceil_div(heads, rope_head_chunk(T, heads, d, kHeadChunk)); }
 
-// Backward: at most this many blocks (their partial rows of dw are summed by one
-// block), four per SM.
+// Backward: at most kBwdBlocks blocks per SM, all at once; each leaves one partial row
+// of dw.
 int64_t bwd_blocks(int64_t T, int heads, int d) {
-  const int64_t n = side_blocks(T, heads, d), most = 4 * (int64_t)sm_count();
+  const int64_t n = ceil_div(side_units(T, heads, d), kBwdThreads / (d / 8));
+  const int64_t most = (int64_t)kBwdBlocks * sm_count();
   return n < most ? n : most;
 }
 
-void fill_side(RopeSide& s, int heads) {
+void fill_side(RopeSide& s, int64_t T, int heads, int d) {
   s.heads = heads;
-  s.chunk = heads < kHeadChunk ? heads : kHeadChunk;
-  s.chunks = heads > 0 ? (int)ceil_div(heads, kHeadChunk) : 1;
+  s.chunk = heads > 0 ? rope_head_chunk(T, heads, d, kHeadChunk) : 1;
+  s.chunks = heads > 0 ? (int)ceil_div(heads, s.chunk) : 1;
 }
 
 template <int D, typename TX, typename TY, int STYLE>
@@ -235,7 +247,7 @@ cudaError_t launch_one(const RopeArgs& a, bool bwd, cudaStream_t stream) {
   const int64_t grid = a.side[0].blocks + a.side[1].blocks;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   return launch_kernel(bwd ? norm_rope_bwd_kernel<D, TX, TY, STYLE> : norm_rope_kernel<D, TX, TY, STYLE>,
-                       dim3((unsigned)grid), dim3(kThreads), 0, stream, false, a);
+                       dim3((unsigned)grid), dim3(bwd ? kBwdThreads : kThreads), 0, stream, false, a);
 }
 
 template <int D>
@@ -271,8 +283,8 @@ int check_rope(int64_t T, int H, int Hk, int d, int x_dtype, int y_dtype, const 
   a.p.style = rot_style;
   a.p.eps = eps;
   a.T = T;
-  fill_side(a.side[0], H);
-  fill_side(a.side[1], Hk);
+  fill_side(a.side[0], T, H, d);
+  fill_side(a.side[1], T, Hk, d);
   a.side[0].x = q, a.side[0].x_stride = q_stride, a.side[0].w = wq;
   a.side[1].x = k, a.side[1].x_stride = k_stride, a.side[1].w = wk;
   return CSA_OK;
@@ -317,7 +329,7 @@ int csa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_s
       if (!in_place && overlap(out[i], on, s.x, span(T, s.x_stride, s.heads, d, x_dtype))) return CSA_ERR_INVALID_ARG;
     }
     a.side[i].y = out[i];
-    a.side[i].blocks = heads[i] > 0 ? side_blocks(T, heads[i], d) : 0;
+    a.side[i].blocks = heads[i] > 0 ? ceil_div(side_units(T, heads[i], d), kThreads / (d / 8)) : 0;
   }
   if (overlap(yq, span(T, (int64_t)H * d, H, d, y_dtype), yk, span(T, (int64_t)Hk * d, Hk, d, y_dtype)))
     return CSA_ERR_INVALID_ARG;
