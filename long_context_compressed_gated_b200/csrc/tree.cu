@@ -195,7 +195,10 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b, bool tell) {
   return q;
 }
 
-__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) { return a / b; }
+// a / b for a >= 0, b > 0; a 64-bit division takes several times a 32-bit one.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 // One segment of a share: part of one item.
 struct Segment {
@@ -439,10 +442,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 32 + lane; b < a.B; b += 32) total += load_seq(a, b, blockIdx.x == 0).total(a.Hk);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    int64_t ctas = total / kMinShare;
-    ctas = ctas < 1 ? 1 : ctas > gridDim.x ? gridDim.x : ctas;
-    const int64_t c = blockIdx.x;
-    int64_t first = c < ctas ? div64(c * total, ctas) : 0, last = c < ctas ? div64((c + 1) * total, ctas) : 0;
+    int64_t ctas = total < (int64_t)gridDim.x * kMinShare ? (int)total / kMinShare : gridDim.x;
+    if (ctas < 1) ctas = 1;
+    // shares of `len` positions, the first `longer` of them one more
+    const int64_t c = blockIdx.x, len = quotient(total, ctas), longer = total - len * ctas;
+    auto share_start = [&](int64_t i) { return i * len + (i < longer ? i : longer); };
+    int64_t first = c < ctas ? share_start(c) : 0, last = c < ctas ? share_start(c + 1) : 0;
     if (skip) first = last = 0;
     int4 split = make_int4(0, 0, 0, 0);
     int b = 0;
@@ -503,8 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       s.b = b;
       s.r0 = q.r0;
       s.n = q.n;
-      s.hk = (int)div64(g - at, head);
-      const int set = (int)div64(g - at - s.hk * head, pair);
+      s.hk = (int)quotient(g - at, head);
+      const int set = (int)quotient(g - at - s.hk * head, pair);
       s.row0 = set * kItemRows;
       const int left = q.n * a.G - s.row0;
       s.rows = left < kItemRows ? left : kItemRows;
@@ -526,8 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       s.slot = t0 == 0 && t1 == q.tiles ? -1 : (int)(2 * c) + (n == 0 ? 0 : 1);
       if (t0 == 0 && t1 < q.tiles) {  // the item goes on in the next CTAs: tell the combine
         const int64_t tail = i0 + kItemCost + (int64_t)wide * (q.tiles - 1);  // its last tile
-        int64_t cl = div64(tail * ctas, total);
-        while (div64((cl + 1) * total, ctas) <= tail) ++cl;
+        const int64_t cl = tail < (len + 1) * longer ? quotient(tail, len + 1) : longer + quotient(tail - (len + 1) * longer, len);
         split = make_int4(s.rows, s.slot, (int)(cl - c + 1), 0);
         // first output row: (r0 * H + hk * G) and the item's rows from row0
         if (lane == 0) {
@@ -731,8 +735,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int jobs = dual ? 2 * (s.t1 - s.t0) : s.t1 - s.t0;
       const int row = trow + (dual && st ? kTile : 0);  // row of the item
       const bool mine = row < s.rows;
-      const int node = mine ? (s.row0 + row) / a.G : 0;
-      const int64_t orow = (int64_t)(s.r0 + node) * a.H + s.hk * a.G + (mine ? (s.row0 + row) % a.G : 0);
+      // its (node, head); the tensors' rows are counted from the sequence's first node and the
+      // key head's first query head, where they fit 32 bits.  A row beyond the item's stands
+      // in for the first: it is computed and never written
+      const int nh = s.row0 + (mine ? row : 0), node = nh / a.G;
+      const int rel = node * a.H + nh - node * a.G;
+      const int64_t row00 = (int64_t)s.r0 * a.H + s.hk * a.G;
       uint64_t mask = 0;
       int lo = 0;
       if (mine) {
@@ -747,13 +755,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int LPR = D / 8, RPW = 32 / LPR;
         const int ch = lane % LPR;
         const uint32_t dst = smem_u32(s_q) + (uint32_t)(st * L::kTileBytes + (ch >> 3) * kHalfBytes);
-        const int64_t off = mine ? orow * D : -1;
+        const __nv_bfloat16* from = a.q + row00 * D + 8 * ch;
         uint4 v[LPR];
 #pragma unroll
-        for (int i = 0; i < LPR; ++i) {
-          const int64_t from = __shfl_sync(0xffffffffu, off, i * RPW + lane / LPR);
-          v[i] = from >= 0 ? *reinterpret_cast<const uint4*>(a.q + from + 8 * ch) : make_uint4(0, 0, 0, 0);
-        }
+        for (int i = 0; i < LPR; ++i)
+          v[i] = *reinterpret_cast<const uint4*>(
+              from + (int64_t)__shfl_sync(0xffffffffu, rel, i * RPW + lane / LPR) * D);
 #pragma unroll
         for (int i = 0; i < LPR; ++i) {
           const int r = (warp & 3) * 32 + i * RPW + lane / LPR;
@@ -886,11 +893,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // rows of this warp, 32 channels at a time: scaled, staged in the shared memory of the
       // warp's own query rows (free now, and no other warp writes there; 16-byte pieces
       // swizzled by row), written out by whole rows
-      const int64_t prow = (int64_t)s.slot * a.part_rows + row;
       const bool part = s.slot >= 0, f32 = part || a.o_f32;
-      const int64_t off = mine ? (part ? prow : orow) * D : -1;
-      float* of = part ? a.part_o : static_cast<float*>(a.O);
-      __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.O);
+      const int64_t out0 = part ? (int64_t)s.slot * a.part_rows : row00;
+      const int to = mine ? (part ? row : rel) : -1;
+      float* of = (part ? a.part_o : static_cast<float*>(a.O)) + out0 * D;
+      __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.O) + out0 * D;
       const int c0 = !dual && st ? D / 2 : 0, c1 = !dual && !st ? D / 2 : D;
       const bool merge = !dual;
       const float w0 = merge || st == 0 ? f[0] : f[1], w1 = merge ? f[1] : 0.f;
@@ -920,9 +927,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {  // 8 lanes a row
               const int r = 4 * i + (lane >> 3), e = lane & 7;
-              const int64_t to = __shfl_sync(0xffffffffu, off, r);
+              const int at = __shfl_sync(0xffffffffu, to, r);
               const float4 v = ld_shared4(stage + r * 128 + ((e ^ (r & 7)) << 4));
-              if (to >= 0) *reinterpret_cast<float4*>(of + to + j + 4 * e) = v;
+              if (at >= 0) *reinterpret_cast<float4*>(of + (int64_t)at * D + j + 4 * e) = v;
             }
           } else {
 #pragma unroll
@@ -936,16 +943,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {  // 4 lanes a row
               const int r = 8 * i + (lane >> 2), e = lane & 3;
-              const int64_t to = __shfl_sync(0xffffffffu, off, r);
+              const int at = __shfl_sync(0xffffffffu, to, r);
               const float4 v = ld_shared4(stage + r * 64 + ((e ^ (r >> 1 & 3)) << 4));
-              if (to >= 0) *reinterpret_cast<float4*>(ob + to + j + 8 * e) = v;
+              if (at >= 0) *reinterpret_cast<float4*>(ob + (int64_t)at * D + j + 8 * e) = v;
             }
           }
         }
       }
       if (mine && (dual || st == 0)) {
-        if (part) a.part_lse[prow] = lse2;
-        else if (a.lse) a.lse[orow] = lse2 * kLn2;
+        if (part) a.part_lse[out0 + row] = lse2;
+        else if (a.lse) a.lse[out0 + rel] = lse2 * kLn2;
       }
       tc_fence_before();
       __syncwarp();
