@@ -11,9 +11,9 @@
 // Up to 256 rows make one item, which walks the keys of its sequence in tiles of
 // 128 from the first one that any row sees.  All items' key tiles, each as long as it
 // takes, form one line, cut into equal shares, one per CTA (one CTA per SM,
-// persistent): lengths may be as ragged as they like.  A share that covers an item only in part writes an
-// fp32 partial (O, lse); tree_combine_kernel merges those.  Lengths are read on
-// the device, so the cut follows them in a captured graph.
+// persistent): lengths may be as ragged as they like.  A share that covers an item
+// only in part writes an fp32 partial (O, lse); tree_combine_kernel merges those.
+// Lengths are read on the device, so the cut follows them in a captured graph.
 //
 // One CTA:
 //   warps 0..3, 4..7  two softmax streams, one thread per row;
@@ -68,10 +68,13 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kMaxNodes = 64;       // bits of a mask
 // Lengths on the line of all items' key tiles, in key tiles of a single row tile (1.0 us;
 // a pair of row tiles takes 2.07 us): a tile of a single row tile, of a pair, and what
-// starting an item costs beside them (outputs written, query rows read: 3.5 us each,
-// partly hidden).
-constexpr int kSingleCost = 1, kPairCost = 2, kItemCost = 4;
-constexpr int kMinShare = kItemCost + 8 * kSingleCost;  // a CTA's share at least
+// starting an item costs beside them (the outputs before it written, query rows read,
+// the pipeline filled).
+constexpr int kSingleCost = 1, kPairCost = 2, kItemCost = 6;
+// A CTA's share at least.  Fewer, longer shares save the merge of partial results where
+// all fit one CTA; beyond that more CTAs win (8 sequences of 1 k .. 8 k rows, 8 drafts
+// each: 41 us with 12 more, 37 with 4 more, 36 with 2 more).
+constexpr int kMinShare = kItemCost + 3 * kSingleCost;
 constexpr float kRescaleSlack = 8.0f;  // raise the running max only when it grows by > 2^8
 constexpr float kLn2 = 0.69314718055994531f;
 

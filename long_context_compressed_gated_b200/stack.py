@@ -11,17 +11,20 @@ Per chunk of C tokens (positions c*C .. c*C+C-1, C a multiple of both ratios):
            heads; outside the method, a torch matmul);
   layer 2  csa_compress appends C/m' entries to the HCA cache, hca_attn attends
            densely to every visible entry plus the window.
+With `position` given, each layer's queries and keys are normed and rotated to
+their positions first (csa_qk_norm_rope; compression then pools positioned keys):
+the inputs are otherwise taken as already positioned.
 Only argument plumbing happens here: every step of the method runs in libcsa.
 """
 import math
 
 import torch
 
-from . import csa_compress, csa_indexer_topk, csa_sparse_attn, hca_attn, lib
+from . import csa_compress, csa_indexer_topk, csa_qk_norm_rope, csa_sparse_attn, hca_attn, lib
 
 
 def stack_prefill_chunked(l1, l2, P, chunk, m, k, W, m2, W2, scale=None, out=None, phase_events=None,
-                          return_o1=False, idx_out=None, scores_out=None):
+                          return_o1=False, idx_out=None, scores_out=None, position=None):
     """Run the two-layer stack over all T tokens in chunks of `chunk`.
 
     l1: dict with Q [T,H,d], K, V, Z [T,d], B [m,d], qI_codes [T,HI,dI/2],
@@ -30,7 +33,9 @@ def stack_prefill_chunked(l1, l2, P, chunk, m, k, W, m2, W2, scale=None, out=Non
     Returns O2 [T,H,d] (and O1 when return_o1).  phase_events: optional list that
     receives (name, start_event, end_event) per phase for timing.  idx_out [T,k]
     int32 / scores_out [T,k] f32 (optional): keep every chunk's layer-1 selection
-    (the indexer writes its rows there instead of a per-chunk buffer).
+    (the indexer writes its rows there instead of a per-chunk buffer).  position:
+    None, or the arguments of csa_qk_norm_rope that both layers share as a dict
+    (inv_freq, optionally wq, wk, eps, rot_start, rot_style).
     """
     Q1 = l1["Q"]
     T, H, d = Q1.shape
@@ -45,6 +50,11 @@ def stack_prefill_chunked(l1, l2, P, chunk, m, k, W, m2, W2, scale=None, out=Non
     O1 = torch.empty_like(Q1)
     Q2 = torch.empty_like(Q1)
     O2 = torch.empty_like(Q1) if out is None else out
+    K1, K2 = l1["K"], l2["K"]
+    if position is not None:
+        # positioned keys of the whole sequence (the windows look back), queries of one chunk
+        K1, K2 = torch.empty_like(K1), torch.empty_like(K2)
+        q_chunk = torch.empty(chunk, H, d, dtype=Q1.dtype, device=dev)
     L = lib()
     HI, dI = l1["qI_scales"].shape[1], l1["qI_scales"].shape[2] * 32
     ws_bytes = max(L.csa_indexer_topk_workspace_bytes(chunk, T // m, HI, dI, k),
@@ -69,21 +79,29 @@ def stack_prefill_chunked(l1, l2, P, chunk, m, k, W, m2, W2, scale=None, out=Non
         idx = idx_chunk if idx_out is None else idx_out[sl]
         sc = None if scores_out is None else scores_out[sl]
         # layer 1 (CSA)
-        timed("compress", lambda: csa_compress(l1["K"][sl], l1["V"][sl], l1["Z"][sl], l1["B"], m, Kc=Kc1[b1:e1],
+        q1 = Q1[sl]
+        if position is not None:
+            q1 = q_chunk
+            timed("position", lambda: csa_qk_norm_rope(Q1[sl], l1["K"][sl].unsqueeze(1), t0=t0, yq=q1,
+                                                       yk=K1[sl].unsqueeze(1), **position))
+        timed("compress", lambda: csa_compress(K1[sl], l1["V"][sl], l1["Z"][sl], l1["B"], m, Kc=Kc1[b1:e1],
                                                Vc=Vc1[b1:e1]))
         timed("indexer_topk", lambda: csa_indexer_topk(l1["qI_codes"][sl], l1["qI_scales"][sl], l1["w_codes"][sl],
                                                        l1["kI_codes"][:e1], l1["kI_scales"][:e1], m, k, t0=t0,
                                                        idx=idx, scores=sc, want_scores=sc is not None,
                                                        workspace=ws))
-        timed("sparse_attn", lambda: csa_sparse_attn(Q1[sl], Kc1[:e1], Vc1[:e1], idx, l1["K"][: t0 + chunk],
+        timed("sparse_attn", lambda: csa_sparse_attn(q1, Kc1[:e1], Vc1[:e1], idx, K1[: t0 + chunk],
                                                      l1["V"][: t0 + chunk], W, scale, t0=t0, O=O1[sl],
                                                      want_lse=False, workspace=ws))
         # glue: per-head projection of the layer-1 output into the layer-2 queries
         timed("projection", lambda: torch.matmul(O1[sl].view(-1, d), P, out=Q2[sl].view(-1, d)))
         # layer 2 (HCA)
-        timed("compress", lambda: csa_compress(l2["K"][sl], l2["V"][sl], l2["Z"][sl], l2["B"], m2, Kc=Kc2[b2:e2],
+        if position is not None:
+            timed("position", lambda: csa_qk_norm_rope(Q2[sl], l2["K"][sl].unsqueeze(1), t0=t0, yq=Q2[sl],
+                                                       yk=K2[sl].unsqueeze(1), **position))
+        timed("compress", lambda: csa_compress(K2[sl], l2["V"][sl], l2["Z"][sl], l2["B"], m2, Kc=Kc2[b2:e2],
                                                Vc=Vc2[b2:e2]))
-        timed("hca_attn", lambda: hca_attn(Q2[sl], Kc2[:e2], Vc2[:e2], l2["K"][: t0 + chunk],
+        timed("hca_attn", lambda: hca_attn(Q2[sl], Kc2[:e2], Vc2[:e2], K2[: t0 + chunk],
                                            l2["V"][: t0 + chunk], m2, W2, scale, t0=t0, O=O2[sl], want_lse=False,
                                            workspace=ws))
     return (O2, O1) if return_o1 else O2
