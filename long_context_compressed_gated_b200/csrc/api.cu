@@ -171,7 +171,7 @@ const char* csa_status_string(int status) {
 
 int csa_last_cuda_error(void) { return g_last_cuda_error; }
 
-int csa_version(void) { return 200; }
+int csa_version(void) { return 300; }
 
 int csa_peak_mma(int kind, int64_t iters, int ctas, void* workspace, size_t workspace_bytes, double* flops,
                  csa_stream_t stream) {

@@ -66,6 +66,7 @@ constexpr int kThreads = 384;       // three warpgroups (the last warp idles)
 // row of S, take 208 and the third group keeps 88 (2 * 208 + 88 = 3 * 168).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kMaxNodes = 64;       // bits of a mask
+constexpr int kMaxSeqs = 65536;     // every CTA adds up all sequences' tiles, within the bound of the other roles' waits
 // Lengths on the line of all items' key tiles, in key tiles of a single row tile (1.0 us;
 // a pair of row tiles takes 2.07 us): a tile of a single row tile, of a pair, and what
 // starting an item costs beside them (the outputs before it written, query rows read,
@@ -1158,7 +1159,8 @@ int csa_tree_attn(const void* q, const void* Kpages, const void* Vpages, const i
   if (R < 0 || R > 0x7FFFFFFF || B < 0 || H < 1 || Hk < 1 || n_pages < 0 || max_pages < 0 || W < -1 ||
       !(std::isfinite(scale) && scale > 0.f) || !valid_odtype(o_dtype))
     return CSA_ERR_INVALID_ARG;
-  if ((d != 64 && d != 128) || !valid_page(page) || H > 1024 || H % Hk != 0) return CSA_ERR_UNSUPPORTED_SHAPE;
+  if ((d != 64 && d != 128) || !valid_page(page) || H > 1024 || H % Hk != 0 || B > kMaxSeqs)
+    return CSA_ERR_UNSUPPORTED_SHAPE;
   if ((int64_t)max_pages * page > 0x7FFFFFFF - kTile || n_pages > 0x7FFFFFFE) return CSA_ERR_UNSUPPORTED_SHAPE;
   int rc = check_ws(workspace, workspace_bytes, csa_tree_attn_workspace_bytes(B, R, H, Hk, d, page, max_pages));
   if (rc) return rc;

@@ -285,13 +285,42 @@ def test_empty_calls(csa):
     assert O.shape == (0, 4, 64)
 
 
-def test_many_sequences(csa):
+@pytest.mark.parametrize("W", [-1, 40])
+def test_many_sequences(csa, W):
     g = torch.Generator().manual_seed(12)
     lens = torch.randint(0, 300, (200,), generator=g).tolist()
     nodes = torch.randint(0, 4, (200,), generator=g).tolist()
     x = make(lens, nodes, 8, 2, 64, 16, seed=13)
-    O, lse, ws = call(csa, x)
-    assert csa.csa_check_status(ws) == 0 and check(x, O, lse).all()
+    O, lse, ws = call(csa, x, W=W)
+    assert csa.csa_check_status(ws) == 0 and check(x, O, lse, W=W).all()
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 16), (128, 256)])
+def test_long_tables(csa, d, page):
+    """More pages than are read ahead at once, from the middle of a run on (window)."""
+    x = make([9000, 4100], [3, 5], 8, 2, d, page, seed=20)
+    for W in (-1, 3333):
+        O, lse, ws = call(csa, x, W=W)
+        assert csa.csa_check_status(ws) == 0 and check(x, O, lse, W=W).all()
+
+
+def test_two_streams_at_once(csa):
+    """Calls that overlap on the GPU, each with its own workspace."""
+    xs = [make([3000, 50, 777], [9, 4, 1], 16, 2, 128, 64, seed=s) for s in (21, 22)]
+    cs = [{k: v.cuda() for k, v in x.items()} for x in xs]
+    want = [call(csa, x)[:2] for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = []
+    for _ in range(20):
+        got = []
+        for c, st in zip(cs, streams):
+            with torch.cuda.stream(st):
+                got.append(csa.csa_tree_attn(c["q"], c["Kp"], c["Vp"], c["table"], c["lens"], c["start"], c["mask"],
+                                             1 / math.sqrt(128), pos=c["pos"])[:2])
+    torch.cuda.synchronize()
+    for (O, l), (wO, wl) in zip(got, want):
+        assert torch.equal(O, wO) and torch.equal(l, wl)
 
 
 def test_partials_combine_with_compressed_entries(csa):

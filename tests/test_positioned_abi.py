@@ -98,7 +98,7 @@ TREE = dict(q=A[0], Kp=A[1], Vp=A[2], table=A[3], lens=A[4], start=A[5], mask=A[
     (dict(R=-1), INV), (dict(R=1 << 31), INV), (dict(B=-1), INV), (dict(H=0), INV), (dict(Hk=0), INV),
     (dict(n_pages=-1), INV), (dict(max_pages=-1), INV), (dict(W=-2), INV), (dict(scale=0.0), INV),
     (dict(scale=float("inf")), INV), (dict(scale=float("nan")), INV), (dict(ot=2), INV), (dict(d=256), SHAPE),
-    (dict(page=24), SHAPE), (dict(H=2048), SHAPE), (dict(Hk=3), SHAPE), (dict(max_pages=1 << 27), SHAPE),
+    (dict(page=24), SHAPE), (dict(H=2048), SHAPE), (dict(Hk=3), SHAPE), (dict(max_pages=1 << 27), SHAPE), (dict(B=65537), SHAPE),
     (dict(ws=None), WS), (dict(wsb=16), WS), (dict(ws=ODD), MIS), (dict(q=None), INV), (dict(Kp=None), INV),
     (dict(Vp=ODD), MIS), (dict(table=None), INV), (dict(lens=None), INV), (dict(start=ODD), MIS), (dict(mask=None), INV),
     (dict(W=4, pos=None), INV), (dict(O=None), INV), (dict(lse=ODD), MIS), (dict(R=0), 0), (dict(B=0), 0)])
