@@ -791,9 +791,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         tc_fence_after();
         if (warp_mine) {
+          // Columns out of sight become -inf where they stand, 32 at a time, before the row is
+          // read (few tiles have any: their code stays small and out of the unrolled part)
+          if (!__all_sync(0xffffffffu, lo <= base && base + kTile <= s.L)) {
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t bits = visible(base + 32 * w, lo, s.L, mask);
+              uint32_t t[32];
+              tmem_ld32p(scol + 32 * w, t);
+              tmem_wait_ld_regs32(t);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(bits >> e & 1)) t[e] = 0xFF800000u;
+              tmem_st32p(scol + 32 * w, t);
+            }
+            tmem_wait_st();
+          }
           // raw logits of the row, 128 columns; the maximum of the first half while the second lands
           uint32_t v[kTile];
-          const bool all = __all_sync(0xffffffffu, lo <= base && base + kTile <= s.L);  // no mask in this tile
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           tmem_ld32p(scol, v);
           tmem_ld32p(scol + 32, v + 32);
@@ -806,15 +821,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (h == 1) {
               tmem_wait_ld_regs32(v + 64);
               tmem_tie32(v + 96);
-            }
-            if (!all) {  // columns out of sight become -inf
-#pragma unroll
-              for (int w = 2 * h; w < 2 * h + 2; ++w) {
-                const uint32_t bits = visible(base + 32 * w, lo, s.L, mask);
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!(bits >> e & 1)) v[32 * w + e] = 0xFF800000u;
-              }
             }
 #pragma unroll
             for (int e = 64 * h; e < 64 * h + 64; e += 2)
