@@ -365,8 +365,9 @@ int csa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_s
  *   dwq, dwk [d] f32 (written, not accumulated; the sums over all tokens and
  *          heads in a fixed order): given exactly when the side and its weight are
  * With T = 0 the weight gradients are zeros.  dq / dk must not overlap q, k, dyq
- * or dyk (CSA_ERR_INVALID_ARG), nor each other's elements.  Deterministic on one GPU model (the split of the sums follows its SM
- * count).  Workspace: csa_qk_norm_rope_backward_workspace_bytes(). */
+ * or dyk (CSA_ERR_INVALID_ARG), nor each other's elements.  Deterministic on one
+ * GPU model (the split of the sums follows its SM count).  Workspace:
+ * csa_qk_norm_rope_backward_workspace_bytes(). */
 size_t csa_qk_norm_rope_backward_workspace_bytes(int64_t T, int H, int Hk, int d);
 int csa_qk_norm_rope_backward(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const float* wq,
                               const float* wk, float eps, const int64_t* pos, int64_t t0, const double* inv_freq,
@@ -430,8 +431,9 @@ int csa_paged_append(const void* k, int64_t k_stride, const void* v, int64_t v_s
  * the rows of that sequence are unspecified.  All of it is read on the device in
  * stream order, so a captured call follows new lengths, tables and masks.
  * d in {64, 128}; page as csa_paged_append; H <= 1024, H % Hk == 0, any ratio;
- * B <= 65536; max_pages * page < 2^31 - 128.  Workspace: csa_tree_attn_workspace_bytes(); calls that
- * can overlap on the GPU need one each. */
+ * B <= 65536; max_pages * page < 2^31 - 128; scale > 0; O must not overlap q
+ * (CSA_ERR_INVALID_ARG).  Workspace: csa_tree_attn_workspace_bytes(); calls that can
+ * overlap on the GPU need one each. */
 size_t csa_tree_attn_workspace_bytes(int B, int64_t R, int H, int Hk, int d, int page, int max_pages);
 int csa_tree_attn(const void* q, const void* Kpages, const void* Vpages, const int32_t* block_table,
                   const int32_t* seq_lens, const int32_t* q_start, const uint64_t* mask, const int64_t* pos, int64_t R,

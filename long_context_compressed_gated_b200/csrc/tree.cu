@@ -160,8 +160,8 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // The first committed row that a node at position pos sees (pos may be anything).
 __device__ __forceinline__ int window_start(int64_t pos, int W, int L) {
-  if (pos < W) return 0;  // pos - W + 1 would be at most 0, or not fit
-  return pos - W + 1 > L ? L : (int)(pos - W + 1);
+  if (pos < W) return 0;  // pos - W + 1 is at most 0
+  return pos - W >= L ? L : (int)(pos - W) + 1;
 }
 
 __device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b, bool tell) {
@@ -1162,8 +1162,9 @@ int csa_tree_attn(const void* q, const void* Kpages, const void* Vpages, const i
                   const int32_t* seq_lens, const int32_t* q_start, const uint64_t* mask, const int64_t* pos, int64_t R,
                   int B, int H, int Hk, int d, int page, int64_t n_pages, int max_pages, int W, float scale, void* O,
                   int o_dtype, float* lse, void* workspace, size_t workspace_bytes, csa_stream_t stream) {
+  const float scale_log2 = scale * 1.4426950408889634f;
   if (R < 0 || R > 0x7FFFFFFF || B < 0 || H < 1 || Hk < 1 || n_pages < 0 || max_pages < 0 || W < -1 ||
-      !(std::isfinite(scale) && scale > 0.f) || !valid_odtype(o_dtype))
+      !(std::isfinite(scale_log2) && scale_log2 > 0.f) || !valid_odtype(o_dtype))
     return CSA_ERR_INVALID_ARG;
   if ((d != 64 && d != 128) || !valid_page(page) || H > 1024 || H % Hk != 0 || B > kMaxSeqs)
     return CSA_ERR_UNSUPPORTED_SHAPE;
@@ -1176,6 +1177,9 @@ int csa_tree_attn(const void* q, const void* Kpages, const void* Vpages, const i
   if (max_pages > 0 && (rc = check_ptrs(block_table))) return rc;
   if (n_pages > 0 && (rc = check_ptrs(Kpages, Vpages))) return rc;
   if ((rc = check_opt(lse))) return rc;
+  // a share writes its outputs while others still read the query rows
+  if (overlap(O, span(R, (int64_t)H * d, H, d, o_dtype), q, span(R, (int64_t)H * d, H, d, CSA_BF16)))
+    return CSA_ERR_INVALID_ARG;
   TreeArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.table = block_table;
@@ -1192,7 +1196,7 @@ int csa_tree_attn(const void* q, const void* Kpages, const void* Vpages, const i
   a.max_pages = max_pages;
   while ((1 << a.page_shift) < page) ++a.page_shift;
   a.W = W;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.O = O;
   a.o_f32 = o_dtype == CSA_F32;
   a.lse = lse;

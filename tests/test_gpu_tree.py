@@ -145,6 +145,14 @@ def test_window(csa, W, lens, nodes, H, Hk, d, page):
     check(x, O, lse, W=W)
 
 
+@pytest.mark.parametrize("W", [0, 3, 2**31 - 1])
+def test_window_at_any_position(csa, W):
+    x = make([300, 40], [5, 3], 8, 2, 64, 16, seed=30)
+    x["pos"][:] = torch.tensor([2**63 - 1, -2**63, 2**62, W, 299 + W, 2**63 - 1, -1, 40 + W])
+    O, lse, ws = call(csa, x, W=W)
+    assert csa.csa_check_status(ws) == 0 and check(x, O, lse, W=W).all()
+
+
 def test_rows_that_see_nothing(csa):
     x = make([0, 40, 0], [4, 3, 70 - 6], 16, 2, 64, 16, seed=5)
     x["mask"][1] = 0            # no key at all

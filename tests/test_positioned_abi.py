@@ -101,7 +101,9 @@ TREE = dict(q=A[0], Kp=A[1], Vp=A[2], table=A[3], lens=A[4], start=A[5], mask=A[
     (dict(page=24), SHAPE), (dict(H=2048), SHAPE), (dict(Hk=3), SHAPE), (dict(max_pages=1 << 27), SHAPE), (dict(B=65537), SHAPE),
     (dict(ws=None), WS), (dict(wsb=16), WS), (dict(ws=ODD), MIS), (dict(q=None), INV), (dict(Kp=None), INV),
     (dict(Vp=ODD), MIS), (dict(table=None), INV), (dict(lens=None), INV), (dict(start=ODD), MIS), (dict(mask=None), INV),
-    (dict(W=4, pos=None), INV), (dict(O=None), INV), (dict(lse=ODD), MIS), (dict(R=0), 0), (dict(B=0), 0)])
+    (dict(W=4, pos=None), INV), (dict(O=None), INV), (dict(lse=ODD), MIS), (dict(R=0), 0), (dict(B=0), 0),
+    (dict(scale=3e38), INV), (dict(O=A[0]), INV), (dict(O=P(0x1000000 + 10224)), INV),
+    (dict(ot=1, q=P(0x9000000 + 20464)), INV)])
 def test_tree_attn_refuses(lib, change, code):
     a = dict(TREE, **change)
     assert lib.csa_tree_attn(*a.values()) == code
