@@ -472,8 +472,8 @@ def _here(*tensors):
 
 
 def _like(x, dtype):
-    """A dense tensor of x's shape on its device."""
-    return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
+    """A dense tensor of the shape of x, whose rows are dense (_rows), on its device."""
+    return torch.empty_like(x) if x.dtype == dtype else torch.empty_like(x, dtype=dtype)
 
 
 def _given(t, dtype, shape, name):
@@ -493,7 +493,7 @@ def _scratch(workspace, device, bytes_needed):
 
 
 def _rows(t, dtypes, name):
-    """Token rows [T, heads, d], each row dense: (elements from row to row, heads)."""
+    """Token rows [T, heads, d], each row dense: (elements from row to row, T, heads, d)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dtype not in dtypes:
@@ -504,7 +504,7 @@ def _rows(t, dtypes, name):
     rs, hs, cs = t.stride()
     if (cs != 1 and d > 1 or hs != d and heads > 1) and t.numel():
         raise ValueError("%s must have dense [heads, d] rows" % name)
-    return (rs if T > 1 else heads * d), heads
+    return (rs if T > 1 else heads * d), T, heads, d
 
 
 def _freq(inv_freq):
@@ -516,14 +516,6 @@ def _freq(inv_freq):
     return inv_freq.data_ptr(), 2 * inv_freq.numel()
 
 
-def _weight(w, d, name):
-    if w is not None:
-        _dev(w, torch.float32, name, 1)
-        if w.numel() != d:
-            raise ValueError("%s must have %d elements" % (name, d))
-    return w
-
-
 def _vector(t, n, dtype, name):
     if t is not None:
         _dev(t, dtype, name, 1)
@@ -532,16 +524,24 @@ def _vector(t, n, dtype, name):
     return t
 
 
+def _weight(w, d, name):
+    return _vector(w, d, torch.float32, name)
+
+
 def _qk_sides(q, k):
+    """(q or k, tokens, query heads, key heads, head dim, the row strides of q and k)"""
     if q is None and k is None:
         raise ValueError("q or k must be given")
-    x = q if q is not None else k
-    qs, H = _rows(q, _ODTYPE, "q") if q is not None else (0, 0)
-    ks, Hk = _rows(k, _ODTYPE, "k") if k is not None else (0, 0)
-    if q is not None and k is not None and (k.dtype != q.dtype or k.shape[0] != q.shape[0] or
-                                            k.shape[2] != q.shape[2]):
-        raise ValueError("q and k must agree in type, tokens and head dim")
-    return x, qs, ks, H, Hk
+    qs = H = ks = Hk = 0
+    if q is not None:
+        qs, T, H, d = _rows(q, _ODTYPE, "q")
+    if k is not None:
+        ks, Tk, Hk, dk = _rows(k, _ODTYPE, "k")
+        if q is None:
+            T, d = Tk, dk
+        elif k.dtype != q.dtype or Tk != T or dk != d:
+            raise ValueError("q and k must agree in type, tokens and head dim")
+    return (k if q is None else q), T, H, Hk, d, qs, ks
 
 
 def csa_qk_norm_rope(q, k, inv_freq, wq=None, wk=None, eps=1e-6, pos=None, t0=0, rot_start=0, rot_style=ROPE_HALVES,
@@ -552,8 +552,7 @@ def csa_qk_norm_rope(q, k, inv_freq, wq=None, wk=None, eps=1e-6, pos=None, t0=0,
     the CPU (None: no rotation), turning channels rot_start .. rot_start + rot.
     pos [T] int64 positions on the device, or None: t0, t0 + 1, ...
     Returns (yq, yk) of out_dtype (default: the inputs' type)."""
-    x, qs, ks, H, Hk = _qk_sides(q, k)
-    T, _, d = x.shape
+    x, T, H, Hk, d, qs, ks = _qk_sides(q, k)
     ot = x.dtype if out_dtype is None else out_dtype
     _weight(wq, d, "wq"), _weight(wk, d, "wk"), _vector(pos, T, torch.int64, "pos")
     fp, rot = _freq(inv_freq)
@@ -577,8 +576,7 @@ def csa_qk_norm_rope_backward(q, k, dyq, dyk, inv_freq, wq=None, wk=None, eps=1e
     """Gradients of csa_qk_norm_rope from dyq/dyk (the types and shapes of yq/yk):
     dq/dk of q's type (given ones may be views of a packed gradient), dwq/dwk [d]
     f32.  Returns (dq, dk, dwq, dwk, workspace), None where there is no input."""
-    x, qs, ks, H, Hk = _qk_sides(q, k)
-    T, _, d = x.shape
+    x, T, H, Hk, d, qs, ks = _qk_sides(q, k)
     _weight(wq, d, "wq"), _weight(wk, d, "wk"), _vector(pos, T, torch.int64, "pos")
     fp, rot = _freq(inv_freq)
     got = dyq if q is not None else dyk
@@ -594,7 +592,7 @@ def csa_qk_norm_rope_backward(q, k, dyq, dyk, inv_freq, wq=None, wk=None, eps=1e
             continue
         _dev(dy, yt, "dy" + n, 3)
         dx = _like(s, s.dtype) if dx is None else dx
-        dxs, _ = _rows(dx, (s.dtype,), "d" + n)
+        dxs = _rows(dx, (s.dtype,), "d" + n)[0]
         if dy.shape != s.shape or dx.shape != s.shape:
             raise ValueError("dy%s and d%s must have shape %s" % (n, n, tuple(s.shape)))
         if w is not None:
@@ -631,10 +629,9 @@ def csa_paged_append(k, v, Kpages, Vpages, block_table, seq, pos, inv_freq, slot
     None: pos; a negative slot skips its token).  Returns the workspace, whose
     status word reports numbers outside their tables."""
     n_pages, Hk, page, d = _paged(Kpages, Vpages, block_table)
-    ks, kh = _rows(k, (torch.bfloat16,), "k")
-    vs, vh = _rows(v, (torch.bfloat16,), "v")
-    T = k.shape[0]
-    if kh != Hk or vh != Hk or k.shape[2] != d or v.shape != k.shape:
+    ks, T, kh, kd = _rows(k, (torch.bfloat16,), "k")
+    vs, Tv, vh, vd = _rows(v, (torch.bfloat16,), "v")
+    if Tv != T or kh != Hk or vh != Hk or kd != d or vd != d:
         raise ValueError("k and v must be [T, %d, %d]" % (Hk, d))
     _vector(seq, T, torch.int32, "seq"), _vector(pos, T, torch.int64, "pos"), _vector(slot, T, torch.int64, "slot")
     _weight(wk, d, "wk")
@@ -669,7 +666,7 @@ def csa_tree_attn(q, Kpages, Vpages, block_table, seq_lens, q_start, mask, scale
     if lse is not None:
         _given(lse, torch.float32, (R, H), "lse")
     elif want_lse:
-        lse = torch.empty(R, H, dtype=torch.float32, device=q.device)
+        lse = q.new_empty((R, H), dtype=torch.float32)
     L = lib()
     _here(q, Kpages, Vpages, block_table, seq_lens, q_start, mask, pos, O, lse, workspace)
     ws = _scratch(workspace, q.device, lambda: L.csa_tree_attn_workspace_bytes(B, R, H, Hk, d, page, max_pages))

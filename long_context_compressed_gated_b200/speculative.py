@@ -22,15 +22,15 @@ def tree_verify_step(qkv, H, Hk, Kpages, Vpages, block_table, seq_lens, q_start,
     zeroed; pass one to read the status, which both kernels report to.  Returns
     O [R, H, d]; lse [R, H] f32 receives the log-sum-exps when given."""
     d = Kpages.shape[3]
-    x = qkv.view(qkv.shape[0], H + 2 * Hk, d)
+    q, k, v = qkv.view(qkv.shape[0], H + 2 * Hk, d).split((H, Hk, Hk), 1)
     if workspace is None:
         B, max_pages = block_table.shape
-        n = lib().csa_tree_attn_workspace_bytes(B, x.shape[0], H, Hk, d, Kpages.shape[2], max_pages)
+        n = lib().csa_tree_attn_workspace_bytes(B, q.shape[0], H, Hk, d, Kpages.shape[2], max_pages)
         workspace = torch.empty(n, dtype=torch.uint8, device=qkv.device)
         workspace[:4].zero_()
     rope = dict(eps=eps, rot_start=rot_start, rot_style=rot_style)
-    q, _ = csa_qk_norm_rope(x[:, :H], None, inv_freq, wq=wq, pos=pos, **rope)
-    csa_paged_append(x[:, H:H + Hk], x[:, H + Hk:], Kpages, Vpages, block_table, seq, pos, inv_freq, slot=slot,
-                     wk=wk, workspace=workspace, **rope)
+    q, _ = csa_qk_norm_rope(q, None, inv_freq, wq=wq, pos=pos, **rope)
+    csa_paged_append(k, v, Kpages, Vpages, block_table, seq, pos, inv_freq, slot=slot, wk=wk, workspace=workspace,
+                     **rope)
     return csa_tree_attn(q, Kpages, Vpages, block_table, seq_lens, q_start, mask, scale, W=W, pos=pos, O=O, lse=lse,
                          want_lse=lse is not None, workspace=workspace, out_dtype=out_dtype)[0]
