@@ -118,8 +118,10 @@ def _ptr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream():
-    dev = torch.cuda.current_device()
+def _stream(dev=None):
+    """The current stream's handle, of the current device (whose number may be given)."""
+    if dev is None:
+        dev = torch.cuda.current_device()
     return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
@@ -464,11 +466,12 @@ def rope_inv_freq(rot_dim, base=10000.0):
 
 
 def _here(*tensors):
-    """Every given tensor is on the current CUDA device."""
+    """Every given tensor is on the current CUDA device, whose number is returned."""
     cur = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != cur:
             raise ValueError("tensors must be on the current CUDA device (cuda:%d), got %s" % (cur, t.device))
+    return cur
 
 
 def _like(x, dtype):
@@ -564,10 +567,10 @@ def csa_qk_norm_rope(q, k, inv_freq, wq=None, wk=None, eps=1e-6, pos=None, t0=0,
         yk = _like(k, ot) if yk is None else _given(yk, ot, k.shape, "yk")
     if q is None and yq is not None or k is None and yk is not None:
         raise ValueError("an output without its input")
-    _here(q, k, wq, wk, pos, yq, yk)
+    dev = _here(q, k, wq, wk, pos, yq, yk)
     _check(lib().csa_qk_norm_rope(_ptr(q), qs, _ptr(k), ks, _ptr(wq), _ptr(wk), eps, _ptr(pos), t0, fp, rot_start, rot,
                                   rot_style, T, H, Hk, d, _ODTYPE[x.dtype], _ptr(yq), _ptr(yk), _ODTYPE[ot],
-                                  _stream()), "csa_qk_norm_rope")
+                                  _stream(dev)), "csa_qk_norm_rope")
     return yq, yk
 
 
@@ -579,35 +582,38 @@ def csa_qk_norm_rope_backward(q, k, dyq, dyk, inv_freq, wq=None, wk=None, eps=1e
     x, T, H, Hk, d, qs, ks = _qk_sides(q, k)
     _weight(wq, d, "wq"), _weight(wk, d, "wk"), _vector(pos, T, torch.int64, "pos")
     fp, rot = _freq(inv_freq)
-    got = dyq if q is not None else dyk
-    if got is None or got.dtype not in _ODTYPE:
+    dy = dyq if q is not None else dyk
+    if dy is None or dy.dtype not in _ODTYPE:
         raise TypeError("the gradients must be torch.bfloat16 or torch.float32")
-    yt = got.dtype
+    yt = dy.dtype
     sides = []
-    for s, dy, dx, w, dw, n in ((q, dyq, dq, wq, dwq, "q"), (k, dyk, dk, wk, dwk, "k")):
+    for s, dy, dx, w, dw, heads, n in ((q, dyq, dq, wq, dwq, H, "q"), (k, dyk, dk, wk, dwk, Hk, "k")):
         if s is None:
             if dy is not None or dx is not None or dw is not None:
                 raise ValueError("gradients of %s without %s" % (n, n))
-            sides.append((None, None, 0, None))
+            sides.append((None, 0, None))
             continue
-        _dev(dy, yt, "dy" + n, 3)
-        dx = _like(s, s.dtype) if dx is None else dx
-        dxs = _rows(dx, (s.dtype,), "d" + n)[0]
-        if dy.shape != s.shape or dx.shape != s.shape:
-            raise ValueError("dy%s and d%s must have shape %s" % (n, n, tuple(s.shape)))
+        shape = (T, heads, d)
+        _given(dy, yt, shape, "dy")
+        if dx is None:
+            dx, stride = _like(s, x.dtype), heads * d
+        else:
+            stride, *got = _rows(dx, (x.dtype,), "dx")
+            if tuple(got) != shape:
+                raise ValueError("d%s must have shape %s" % (n, shape))
         if w is not None:
-            dw = torch.empty_like(w) if dw is None else _weight(dw, d, "dw" + n)
+            dw = torch.empty_like(w) if dw is None else _weight(dw, d, "dw")
         elif dw is not None:
             raise ValueError("dw%s without w%s" % (n, n))
-        sides.append((dy, dx, dxs, dw))
-    (dyq, dq, dqs, dwq), (dyk, dk, dks, dwk) = sides
+        sides.append((dx, stride, dw))
+    (dq, dqs, dwq), (dk, dks, dwk) = sides
     L = lib()
-    _here(q, k, wq, wk, pos, dyq, dyk, dq, dk, dwq, dwk, workspace)
+    dev = _here(q, k, wq, wk, pos, dyq, dyk, dq, dk, dwq, dwk, workspace)
     ws = _scratch(workspace, x.device, lambda: L.csa_qk_norm_rope_backward_workspace_bytes(T, H, Hk, d))
     _check(L.csa_qk_norm_rope_backward(_ptr(q), qs, _ptr(k), ks, _ptr(wq) if H else None, _ptr(wk) if Hk else None,
                                        eps, _ptr(pos), t0, fp, rot_start, rot, rot_style, _ptr(dyq), _ptr(dyk), T, H,
                                        Hk, d, _ODTYPE[x.dtype], _ODTYPE[yt], _ptr(dq), dqs, _ptr(dk), dks, _ptr(dwq),
-                                       _ptr(dwk), _ptr(ws), ws.numel(), _stream()), "csa_qk_norm_rope_backward")
+                                       _ptr(dwk), _ptr(ws), ws.numel(), _stream(dev)), "csa_qk_norm_rope_backward")
     return dq, dk, dwq, dwk, ws
 
 
@@ -636,12 +642,12 @@ def csa_paged_append(k, v, Kpages, Vpages, block_table, seq, pos, inv_freq, slot
     _vector(seq, T, torch.int32, "seq"), _vector(pos, T, torch.int64, "pos"), _vector(slot, T, torch.int64, "slot")
     _weight(wk, d, "wk")
     fp, rot = _freq(inv_freq)
-    _here(k, v, Kpages, Vpages, block_table, seq, pos, slot, wk, workspace)
+    dev = _here(k, v, Kpages, Vpages, block_table, seq, pos, slot, wk, workspace)
     ws = _scratch(workspace, k.device, lambda: 256)
     _check(lib().csa_paged_append(_ptr(k), ks, _ptr(v), vs, _ptr(wk), eps, _ptr(pos), _ptr(slot), _ptr(seq), fp,
                                   rot_start, rot, rot_style, _ptr(block_table), T, Hk, d, block_table.shape[0],
                                   block_table.shape[1], n_pages, page, _ptr(Kpages), _ptr(Vpages), _ptr(ws),
-                                  ws.numel(), _stream()), "csa_paged_append")
+                                  ws.numel(), _stream(dev)), "csa_paged_append")
     return ws
 
 
@@ -668,9 +674,9 @@ def csa_tree_attn(q, Kpages, Vpages, block_table, seq_lens, q_start, mask, scale
     elif want_lse:
         lse = q.new_empty((R, H), dtype=torch.float32)
     L = lib()
-    _here(q, Kpages, Vpages, block_table, seq_lens, q_start, mask, pos, O, lse, workspace)
+    dev = _here(q, Kpages, Vpages, block_table, seq_lens, q_start, mask, pos, O, lse, workspace)
     ws = _scratch(workspace, q.device, lambda: L.csa_tree_attn_workspace_bytes(B, R, H, Hk, d, page, max_pages))
     _check(L.csa_tree_attn(_ptr(q), _ptr(Kpages), _ptr(Vpages), _ptr(block_table), _ptr(seq_lens), _ptr(q_start),
                            _ptr(mask), _ptr(pos), R, B, H, Hk, d, page, n_pages, max_pages, W, scale, _ptr(O),
-                           _ODTYPE[out_dtype], _ptr(lse), _ptr(ws), ws.numel(), _stream()), "csa_tree_attn")
+                           _ODTYPE[out_dtype], _ptr(lse), _ptr(ws), ws.numel(), _stream(dev)), "csa_tree_attn")
     return O, lse, ws
