@@ -185,7 +185,7 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b, bool tell) {
   q.S = q.L + q.n;
   if (a.W >= 0) {
     int64_t p = a.pos[q.r0];
-#pragma unroll 2
+#pragma unroll 8
     for (int i = 1; i < q.n; ++i) {
       const int64_t x = a.pos[q.r0 + i];
       p = x < p ? x : p;
