@@ -24,7 +24,7 @@
 // every K/V tile; a smaller item gives both streams the same rows and alternate
 // key tiles.  Either way one stream's softmax runs while the tensor pipe works on
 // the other's tile.  Per stream and key tile: S = Q K^T (tcgen05, fp32 in TMEM),
-// online softmax with the whole row in one thread's registers, P as bf16 back
+// online softmax with one thread a row, P as bf16 back
 // over S's columns, O += P V with A = P from TMEM.  The tensor pipe runs one
 // thread's products in the order of issue, so S of a stream's next tile may be
 // issued right behind the PV that reads the P in the same columns, and a
@@ -68,10 +68,7 @@ constexpr int kTile = 128;          // rows of a tensor tile, keys of a key tile
 constexpr int kItemRows = 2 * kTile;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kLoadWarp2 = 10;
-constexpr int kThreads = 384;       // three warpgroups (the last warp idles)
-// Registers: 384 threads launch with 168 each; the softmax groups, which hold a
-// row of S, take 208 and the third group keeps 88 (2 * 208 + 88 = 3 * 168).
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kThreads = 352;       // 11 warps, up to 168 registers a thread
 constexpr int kMaxNodes = 64;       // bits of a mask
 constexpr int kMaxSeqs = 65536;     // every CTA adds up all sequences' tiles, within the bound of the other roles' waits
 // Lengths on the line of all items' key tiles, in key tiles of a single row tile (1.0 us;
@@ -440,7 +437,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == kLoadWarp) {
-    regs_decrease<kOtherRegs>();
     // =========================== the share: its segments and their K / V tiles
     griddep_launch_dependents();
     // what every sequence asks for, 32 of them at a time (lane: sequence block + lane); the
@@ -576,7 +572,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     drain();
   } else if (warp == kMmaWarp) {
-    regs_decrease<kOtherRegs>();
     // =========================== MMA issue
     // The tensor pipe runs dry whenever this warp's scalar work between two products is
     // longer than the products that are queued, so the loop is kept short: streams and
@@ -717,7 +712,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit_if(leader, mma_fin);
     mbar_wait(mma_fin, 0);
   } else if (warp == kLoadWarp2) {
-    regs_decrease<kOtherRegs>();
     // =========================== the other half of the K / V tiles
 #pragma unroll 1
     for (int n = 0;; ++n) {
@@ -726,10 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       release_segment(n);
     }
     drain();
-  } else if (warp > kLoadWarp2) {
-    regs_decrease<kOtherRegs>();
   } else {
-    regs_increase<kSoftmaxRegs>();
     // =========================== softmax streams (warps 0..3, 4..7): one row per thread
     const int st = warp >> 2;
     const int trow = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
@@ -814,23 +805,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_wait_st();
           }
-          // raw logits of the row, 128 columns; the maximum of the first half while the second lands
-          uint32_t v[kTile];
+          // raw logits of the row, read in two halves and, but for the first, again for the weights:
+          // the loop's code stays small (the warps of a quarter of the SM are in different places
+          // of it and wait for instructions otherwise), and half a row fits the 168 registers of
+          // a thread.  The whole row in registers took 200 us for drafted trees (190 now)
+          uint32_t v[64];
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          tmem_ld32p(scol, v);
-          tmem_ld32p(scol + 32, v + 32);
-          tmem_wait_ld_regs32(v);
-          tmem_tie32(v + 32);
-          tmem_ld32p(scol + 64, v + 64);
-          tmem_ld32p(scol + 96, v + 96);
+#pragma unroll 1
+          for (int h = 64; h >= 0; h -= 64) {
+            tmem_ld32p(scol + h, v);
+            tmem_ld32p(scol + h + 32, v + 32);
+            tmem_wait_ld_regs32(v);
+            tmem_tie32(v + 32);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h == 1) {
-              tmem_wait_ld_regs32(v + 64);
-              tmem_tie32(v + 96);
-            }
-#pragma unroll
-            for (int e = 64 * h; e < 64 * h + 64; e += 2)
+            for (int e = 0; e < 64; e += 2)
               mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
           }
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
@@ -853,13 +841,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           m_run = m_new;
           // p = 2^(s c - m); the sums take the unrounded weights, the product with V
-          // their bf16 rounding (the tensor pipe's operand type)
-#pragma unroll
+          // their bf16 rounding (the tensor pipe's operand type).  P of the first half covers
+          // columns 0 .. 31, so the second half's logits still stand
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             uint32_t pk[32];
 #pragma unroll
             for (int e = 0; e < 64; e += 2) {
-              float2 z = fma2(make_float2(__uint_as_float(v[64 * h + e]), __uint_as_float(v[64 * h + e + 1])), both(c),
+              float2 z = fma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), both(c),
                               both(-m_use));
               z.x = fast_exp2(z.x), z.y = fast_exp2(z.y);
               l2 = add2(l2, z);
@@ -867,10 +856,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_st32p(scol + 32 * h, pk);
             if (h == 0) {
+              tmem_ld32p(scol + 64, v);
+              tmem_ld32p(scol + 96, v + 32);
               tmem_wait_st();
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(&p_full[2 * st]);
+              tmem_wait_ld_regs32(v);
+              tmem_tie32(v + 32);
             }
           }
           tmem_wait_st();
