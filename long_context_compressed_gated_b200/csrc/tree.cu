@@ -278,6 +278,19 @@ __device__ __forceinline__ uint32_t visible(int off, int lo, int L, uint64_t mas
   return w;
 }
 
+// The rest of a bounded wait, out of line: the waits' code stays small.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* aborted, int* status) {
+  const long long start = clock64();
+  while (!*aborted) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (clock64() - start > CSA_WAIT_CYCLES) {
+      report(status, CSA_ERR_DEVICE_TIMEOUT);
+      *aborted = 1;
+    }
+  }
+  return false;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_attn_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ TreeMaps maps) {
@@ -342,15 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Bounded wait that also stops once any role of this CTA has given up.
   auto wait = [&](uint64_t* b_, uint32_t ph) -> bool {
     if (mbar_try_wait(b_, ph)) return true;
-    const long long start = clock64();
-    while (!*s_abort) {
-      if (mbar_try_wait(b_, ph)) return true;
-      if (clock64() - start > CSA_WAIT_CYCLES) {
-        report(a.status, CSA_ERR_DEVICE_TIMEOUT);
-        *s_abort = 1;
-      }
-    }
-    return false;
+    return wait_on(b_, ph, s_abort, a.status);
   };
   // the next segment's description (in place until the role releases it), or null
   auto next_segment = [&](int n) -> const Segment* {
