@@ -43,12 +43,19 @@ namespace {
 
 constexpr int kThreads = 256;      // forward
 constexpr int kAhead = 4;          // rows of a group loaded before the first is used
-// Backward: the bytes in flight are limited by its registers.  Measured on 16384 tokens of
-// 65 heads of 128 (bf16, with the sum of dw; the bytes alone take 125 us): 151 us with five
-// blocks of 128 threads per SM, 157 with three of 256, 168 with two of 256, 175 with four
-// of 256 (one row ahead); fetching the next unit's rows into L2 ahead: 198.
-constexpr int kBwdThreads = 128, kBwdBlocks = 5, kBwdAhead = 2;
-constexpr int kHeadChunk = 16;     // most heads of one token that share a set of coefficients
+// Backward: the bytes in flight are limited by its registers.  Blocks of 128 threads per SM
+// and rows of a group ahead, by types; 600 MB of 65 heads of 128, with the sum of dw (the
+// bytes alone take 92 us): bf16 five and two 117, four and three 131, six and two 142 us;
+// fp32 four and three 106, five and two 134, three and four 113; mixed four and three 112.
+constexpr int kBwdThreads = 128;
+constexpr bool bwd_wide(int bytes_x, int bytes_y) { return bytes_x + bytes_y > 4; }
+constexpr int bwd_blocks_per_sm(bool wide) { return wide ? 4 : 5; }
+// Most heads of one token that share a set of coefficients: fewer sets with 16, shorter pieces
+// of memory with 8.  Forward, 600 MB: bf16 outputs 102 against 115 us with 8, fp32 outputs
+// 98 against 94; backward: bf16 118 against 128, with an fp32 side 106 against 100.
+constexpr int head_chunk_most(bool wide) { return wide ? 8 : 16; }
+// What a unit costs beside its rows (its token's coefficients, the first loads), in rows.
+constexpr int kUnitRows = 2;
 
 // Queries or keys of one call.
 struct RopeSide {
@@ -117,9 +124,9 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
 // of dw in registers, and the block adds its groups' shares in order: one partial
 // row per block, summed in order by norm_rope_dw_kernel (no atomics).
 template <int D, typename TX, typename TY, int STYLE>
-__global__ void __launch_bounds__(kBwdThreads, kBwdBlocks)
+__global__ void __launch_bounds__(kBwdThreads, bwd_blocks_per_sm(bwd_wide(sizeof(TX), sizeof(TY))))
     norm_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int LPR = D / 8, GROUPS = kBwdThreads / LPR;
+  constexpr int LPR = D / 8, GROUPS = kBwdThreads / LPR, kBwdAhead = bwd_wide(sizeof(TX), sizeof(TY)) ? 3 : 2;
   __shared__ uint64_t s_turn[kRopeMaxPairs];
   __shared__ float s_dw[GROUPS * D];
   stage_turns(a.p, s_turn);
@@ -203,42 +210,62 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks)
   }
 }
 
-// dw = sum of a side's partial rows: block 0 the queries', block 1 the keys';
-// 8 threads per channel take every eighth row, then add up in order.
+// dw = sum of a side's partial rows (blockIdx.y 0 the queries', 1 the keys'), 32 channels a
+// block: its warps take every 32nd row each, then their sums are added in order.  (Two blocks,
+// eight rows at a time, took 3 us more of a call with 740 rows a side.)
+constexpr int kDwWarps = 32;
+
 template <int D>
-__global__ void __launch_bounds__(8 * D) norm_rope_dw_kernel(const float* part, int64_t qblocks, int64_t kblocks,
-                                                             float* dwq, float* dwk) {
+__global__ void __launch_bounds__(32 * kDwWarps) norm_rope_dw_kernel(const float* part, int64_t qblocks,
+                                                                     int64_t kblocks, float* dwq, float* dwk) {
   griddep_wait();
-  float* dw = blockIdx.x ? dwk : dwq;
+  float* dw = blockIdx.y ? dwk : dwq;
   if (dw == nullptr) return;
-  const int64_t n = blockIdx.x ? kblocks : qblocks;
-  const float* p = part + (blockIdx.x ? qblocks * D : 0);
-  __shared__ float s[8 * D];
-  const int c = threadIdx.x % D, g = threadIdx.x / D;
+  const int64_t n = blockIdx.y ? kblocks : qblocks;
+  const float* p = part + (blockIdx.y ? qblocks * D : 0);
+  __shared__ float s[kDwWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float sum = 0.f;
 #pragma unroll 8
-  for (int64_t i = g; i < n; i += 8) sum += p[i * D + c];
-  s[g * D + c] = sum;
+  for (int64_t i = warp; i < n; i += kDwWarps) sum += p[i * D + c];
+  s[warp][lane] = sum;
   __syncthreads();
-  if (g == 0) {
-    for (int i = 1; i < 8; ++i) sum += s[i * D + c];
+  if (warp == 0) {
+#pragma unroll
+    for (int i = 1; i < kDwWarps; ++i) sum += s[i][lane];
     dw[c] = sum;
   }
 }
 
-int64_t side_units(int64_t T, int heads, int d) { return T * ceil_div(heads, rope_head_chunk(T, heads, d, kHeadChunk)); }
-
-// Backward: at most kBwdBlocks blocks per SM, all at once; each leaves one partial row
-// of dw.
-int64_t bwd_blocks(int64_t T, int heads, int d) {
-  const int64_t n = ceil_div(side_units(T, heads, d), kBwdThreads / (d / 8));
-  const int64_t most = (int64_t)kBwdBlocks * sm_count();
-  return n < most ? n : most;
+int64_t side_units(int64_t T, int heads, int d, bool wide) {
+  return T * ceil_div(heads, rope_head_chunk(T, heads, d, head_chunk_most(wide)));
 }
 
-void fill_side(RopeSide& s, int64_t T, int heads, int d) {
+// Blocks of the queries and of the keys in the backward pass: all at once on the GPU, each
+// with its share of the work; each leaves one partial row of dw.
+void bwd_split(int64_t T, int H, int Hk, int d, bool wide, int64_t* blocks) {
+  const int heads[2] = {H, Hk};
+  int64_t need[2] = {0, 0}, work[2] = {0, 0};
+  for (int i = 0; i < 2; ++i) {
+    if (heads[i] <= 0) continue;
+    const int64_t units = side_units(T, heads[i], d, wide);
+    need[i] = ceil_div(units, kBwdThreads / (d / 8));
+    work[i] = T * heads[i] + units * kUnitRows;
+  }
+  const int64_t most = (int64_t)bwd_blocks_per_sm(wide) * sm_count();
+  blocks[0] = need[0], blocks[1] = need[1];
+  if (need[0] + need[1] <= most) return;
+  int64_t k = (int64_t)((double)most * work[1] / (work[0] + work[1]) + 0.5);
+  if (k < 1) k = 1;
+  if (k > most - 1 && H > 0) k = most - 1;
+  if (k > need[1]) k = need[1];
+  blocks[0] = need[0] < most - k ? need[0] : most - k;
+  blocks[1] = need[1] < most - blocks[0] ? need[1] : most - blocks[0];
+}
+
+void fill_side(RopeSide& s, int64_t T, int heads, int d, bool wide) {
   s.heads = heads;
-  s.chunk = heads > 0 ? rope_head_chunk(T, heads, d, kHeadChunk) : 1;
+  s.chunk = heads > 0 ? rope_head_chunk(T, heads, d, head_chunk_most(wide)) : 1;
   s.chunks = heads > 0 ? (int)ceil_div(heads, s.chunk) : 1;
 }
 
@@ -265,7 +292,7 @@ cudaError_t launch_types(const RopeArgs& a, int xt, int yt, bool bwd, cudaStream
 // Arguments that forward and backward share.
 int check_rope(int64_t T, int H, int Hk, int d, int x_dtype, int y_dtype, const void* q, int64_t q_stride,
                const void* k, int64_t k_stride, const float* wq, const float* wk, float eps,
-               const double* inv_freq, int rot_start, int rot_dim, int rot_style, RopeArgs& a) {
+               const double* inv_freq, int rot_start, int rot_dim, int rot_style, bool wide, RopeArgs& a) {
   if (T < 0 || H < 0 || Hk < 0 || H > 4096 || Hk > 4096 || !valid_odtype(x_dtype) || !valid_odtype(y_dtype))
     return CSA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return CSA_ERR_UNSUPPORTED_SHAPE;
@@ -283,8 +310,8 @@ int check_rope(int64_t T, int H, int Hk, int d, int x_dtype, int y_dtype, const 
   a.p.style = rot_style;
   a.p.eps = eps;
   a.T = T;
-  fill_side(a.side[0], T, H, d);
-  fill_side(a.side[1], T, Hk, d);
+  fill_side(a.side[0], T, H, d, wide);
+  fill_side(a.side[1], T, Hk, d, wide);
   a.side[0].x = q, a.side[0].x_stride = q_stride, a.side[0].w = wq;
   a.side[1].x = k, a.side[1].x_stride = k_stride, a.side[1].w = wk;
   return CSA_OK;
@@ -311,8 +338,9 @@ int csa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_s
                      int rot_start, int rot_dim, int rot_style, int64_t T, int H, int Hk, int d, int x_dtype,
                      void* yq, void* yk, int y_dtype, csa_stream_t stream) {
   RopeArgs a{};
+  const bool wide = y_dtype == CSA_F32;
   int rc = check_rope(T, H, Hk, d, x_dtype, y_dtype, q, q_stride, k, k_stride, wq, wk, eps, inv_freq, rot_start,
-                      rot_dim, rot_style, a);
+                      rot_dim, rot_style, wide, a);
   if (rc) return rc;
   if ((rc = check_opt(pos))) return rc;
   if (T == 0 || (H == 0 && Hk == 0)) return CSA_OK;
@@ -329,7 +357,7 @@ int csa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_s
       if (!in_place && overlap(out[i], on, s.x, span(T, s.x_stride, s.heads, d, x_dtype))) return CSA_ERR_INVALID_ARG;
     }
     a.side[i].y = out[i];
-    a.side[i].blocks = heads[i] > 0 ? ceil_div(side_units(T, heads[i], d), kThreads / (d / 8)) : 0;
+    a.side[i].blocks = heads[i] > 0 ? ceil_div(side_units(T, heads[i], d, wide), kThreads / (d / 8)) : 0;
   }
   if (overlap(yq, span(T, (int64_t)H * d, H, d, y_dtype), yk, span(T, (int64_t)Hk * d, Hk, d, y_dtype)))
     return CSA_ERR_INVALID_ARG;
@@ -342,8 +370,12 @@ int csa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_s
 
 size_t csa_qk_norm_rope_backward_workspace_bytes(int64_t T, int H, int Hk, int d) {
   if (T <= 0 || d <= 0) return kWorkspaceHeader;
-  const int64_t rows = (H > 0 ? bwd_blocks(T, H, d) : 0) + (Hk > 0 ? bwd_blocks(T, Hk, d) : 0);
-  return kWorkspaceHeader + align256((size_t)rows * d * 4);
+  int64_t most = 0, blocks[2];
+  for (bool wide : {false, true}) {  // whatever the types
+    bwd_split(T, H, Hk, d, wide, blocks);
+    if (blocks[0] + blocks[1] > most) most = blocks[0] + blocks[1];
+  }
+  return kWorkspaceHeader + align256((size_t)most * d * 4);
 }
 
 int csa_qk_norm_rope_backward(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const float* wq,
@@ -353,8 +385,9 @@ int csa_qk_norm_rope_backward(const void* q, int64_t q_stride, const void* k, in
                               int64_t dk_stride, float* dwq, float* dwk, void* workspace, size_t workspace_bytes,
                               csa_stream_t stream) {
   RopeArgs a{};
+  const bool wide = bwd_wide(x_dtype == CSA_BF16 ? 2 : 4, y_dtype == CSA_BF16 ? 2 : 4);
   int rc = check_rope(T, H, Hk, d, x_dtype, y_dtype, q, q_stride, k, k_stride, wq, wk, eps, inv_freq, rot_start,
-                      rot_dim, rot_style, a);
+                      rot_dim, rot_style, wide, a);
   if (rc) return rc;
   if ((rc = check_opt(pos))) return rc;
   if ((H > 0 && wq != nullptr) != (dwq != nullptr) || (Hk > 0 && wk != nullptr) != (dwk != nullptr))
@@ -377,6 +410,8 @@ int csa_qk_norm_rope_backward(const void* q, int64_t q_stride, const void* k, in
     return e == cudaSuccess ? CSA_OK : cuda_fail(e);
   }
   if (H == 0 && Hk == 0) return CSA_OK;
+  int64_t blocks[2];
+  bwd_split(T, H, Hk, d, wide, blocks);
   for (int i = 0; i < 2; ++i) {
     if (heads[i] == 0) continue;
     if ((rc = check_ptrs(dy[i], dx[i]))) return rc;
@@ -389,7 +424,7 @@ int csa_qk_norm_rope_backward(const void* q, int64_t q_stride, const void* k, in
     a.side[i].dy = dy[i];
     a.side[i].dx = dx[i];
     a.side[i].dx_stride = dxs[i];
-    a.side[i].blocks = bwd_blocks(T, heads[i], d);
+    a.side[i].blocks = blocks[i];
   }
   a.p.pos = pos;
   a.p.t0 = t0;
@@ -397,8 +432,8 @@ int csa_qk_norm_rope_backward(const void* q, int64_t q_stride, const void* k, in
   cudaError_t e = d == 128 ? launch_types<128>(a, x_dtype, y_dtype, true, s)
                            : launch_types<64>(a, x_dtype, y_dtype, true, s);
   if (e == cudaSuccess && (dwq || dwk))
-    e = launch_kernel(d == 128 ? norm_rope_dw_kernel<128> : norm_rope_dw_kernel<64>, dim3(2), dim3(8 * d), 0, s, true,
-                      (const float*)a.dw_part, a.side[0].blocks, a.side[1].blocks, dwq, dwk);
+    e = launch_kernel(d == 128 ? norm_rope_dw_kernel<128> : norm_rope_dw_kernel<64>, dim3(d / 32, 2),
+                      dim3(32 * kDwWarps), 0, s, true, (const float*)a.dw_part, a.side[0].blocks, a.side[1].blocks, dwq, dwk);
   return e == cudaSuccess ? CSA_OK : cuda_fail(e);
 }
 
