@@ -142,6 +142,31 @@ def test_backward(csa, T, H, Hk, d, rot, start, style, dtype, out, packed, t0, n
             assert got[2 + i] is None
 
 
+@pytest.mark.parametrize("H,Hk,d,dtype,out", [(9, 2, 64, F32, F32), (17, 1, 128, BF, BF), (3, 3, 64, BF, F32)])
+def test_backward_of_long_calls(csa, H, Hk, d, dtype, out):
+    """More rows than the GPU's blocks take at once: each side with the other and alone, against
+    short calls.  dx is the same row by row; dw adds up in another order: both are within
+    rows * u of the sum of its terms' sizes, bounded by Cauchy-Schwarz per channel."""
+    T, cut = 20011, 1009
+    q, k, wq, wk, qd, kd = make(T, H, Hk, d, dtype, False, seed=12)
+    g = torch.Generator().manual_seed(13)
+    dq, dk = (torch.randn(T, n, d, generator=g).to(out).cuda() for n in (H, Hk))
+    f, w = csa.rope_inv_freq(32), dict(wq=wq.cuda(), wk=wk.cuda())
+    both = csa.csa_qk_norm_rope_backward(qd, kd, dq, dk, f, **w)
+    alone = [csa.csa_qk_norm_rope_backward(qd, None, dq, None, f, wq=w["wq"]),
+             csa.csa_qk_norm_rope_backward(None, kd, None, dk, f, wk=w["wk"])]
+    parts = [csa.csa_qk_norm_rope_backward(qd[t:t + cut], kd[t:t + cut], dq[t:t + cut], dk[t:t + cut], f, t0=t, **w)
+             for t in range(0, T, cut)]
+    for i, (x, dy, n) in enumerate(((q, dq, H), (k, dk, Hk))):
+        assert torch.equal(both[i], alone[i][i]) and torch.equal(both[i], torch.cat([p[i] for p in parts]))
+        want = sum(p[2 + i].double() for p in parts)
+        xh = x.double() * (x.double().square().mean(-1, keepdim=True) + EPS).rsqrt()
+        e = dy.cpu().double().square().sum((0, 1))   # a channel of g mixes its own and its partner's dy
+        size = ((e + e.max()) * xh.square().sum((0, 1))).sqrt().cuda()
+        for dw in (both[2 + i], alone[i][2 + i]):
+            assert ((dw.double() - want).abs() <= 2 * (T * n + 84) * ref.U * size).all()
+
+
 def test_gradient_against_differences(csa):
     """Directional differences of the fp32 kernel itself.  h = 2^-7: the truncation
     is h^2/6 of the third derivative (the norm's, of order |v|^3 |y| / |x|^2 a row), the
