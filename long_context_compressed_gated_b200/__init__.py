@@ -465,13 +465,23 @@ def rope_inv_freq(rot_dim, base=10000.0):
     return float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
 
 
-def _here(*tensors):
-    """Every given tensor is on the current CUDA device, whose number is returned."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != cur:
-            raise ValueError("tensors must be on the current CUDA device (cuda:%d), got %s" % (cur, t.device))
-    return cur
+def _device(t, name):
+    """The device number of a call: its first tensor's, which is the current one."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError("%s must be on the current CUDA device (cuda:%d), got %s" %
+                         (name, torch.cuda.current_device(), t.device))
+    return dev
+
+
+def _on(t, dev, name):
+    """t is on the call's device, too."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the current CUDA device (cuda:%d), got %s" % (name, dev, t.device))
 
 
 def _like(x, dtype):
@@ -479,31 +489,59 @@ def _like(x, dtype):
     return torch.empty_like(x) if x.dtype == dtype else torch.empty_like(x, dtype=dtype)
 
 
-def _given(t, dtype, shape, name):
-    """An output that the caller supplies."""
-    _dev(t, dtype, name)
-    if t.shape != shape:
+def _dense(t, dtype, ndim, name, dev):
+    """A contiguous tensor of the call: its shape."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _on(t, dev, name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    shape = t.shape
+    if len(shape) != ndim:
+        raise ValueError("%s must have %d dims, got %d" % (name, ndim, len(shape)))
+    return shape
+
+
+def _given(t, dtype, shape, name, dev):
+    """A tensor of a known shape, an output that the caller supplies above all."""
+    if _dense(t, dtype, len(shape), name, dev) != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     return t
 
 
-def _scratch(workspace, device, bytes_needed):
+def _vector(t, n, dtype, name, dev):
+    """n elements, or None: the address."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _on(t, dev, name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must have %d elements in one dense dim, got %s" % (name, n, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _scratch(workspace, dev, bytes_needed):
     """The caller's workspace (its size is checked by the library), or a new one of
     bytes_needed() bytes with a clear status word."""
     if workspace is not None:
-        return _dev(workspace, torch.uint8, "workspace")
-    return _workspace(bytes_needed(), device)
+        _dense(workspace, torch.uint8, 1, "workspace", dev)
+        return workspace
+    return _workspace(bytes_needed(), torch.device("cuda", dev))
 
 
-def _rows(t, dtypes, name):
+def _rows(t, dtypes, name, dev):
     """Token rows [T, heads, d], each row dense: (elements from row to row, T, heads, d)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA tensor" % name)
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _on(t, dev, name)
     if t.dtype not in dtypes:
         raise TypeError("%s must be one of %s, got %s" % (name, tuple(dtypes), t.dtype))
-    if t.dim() != 3:
-        raise ValueError("%s must have 3 dims, got %d" % (name, t.dim()))
-    T, heads, d = t.shape
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError("%s must have 3 dims, got %d" % (name, len(shape)))
+    T, heads, d = shape
     rs, hs, cs = t.stride()
     if (cs != 1 and d > 1 or hs != d and heads > 1) and t.numel():
         raise ValueError("%s must have dense [heads, d] rows" % name)
@@ -519,32 +557,23 @@ def _freq(inv_freq):
     return inv_freq.data_ptr(), 2 * inv_freq.numel()
 
 
-def _vector(t, n, dtype, name):
-    if t is not None:
-        _dev(t, dtype, name, 1)
-        if t.numel() != n:
-            raise ValueError("%s must have %d elements, got %d" % (name, n, t.numel()))
-    return t
-
-
-def _weight(w, d, name):
-    return _vector(w, d, torch.float32, name)
-
-
 def _qk_sides(q, k):
-    """(q or k, tokens, query heads, key heads, head dim, the row strides of q and k)"""
+    """(device number, type, tokens, query heads, key heads, head dim, row strides of q and k)"""
     if q is None and k is None:
         raise ValueError("q or k must be given")
     qs = H = ks = Hk = 0
     if q is not None:
-        qs, T, H, d = _rows(q, _ODTYPE, "q")
+        dev, dtype = _device(q, "q"), q.dtype
+        qs, T, H, d = _rows(q, _ODTYPE, "q", dev)
     if k is not None:
-        ks, Tk, Hk, dk = _rows(k, _ODTYPE, "k")
+        if q is None:
+            dev, dtype = _device(k, "k"), k.dtype
+        ks, Tk, Hk, dk = _rows(k, _ODTYPE, "k", dev)
         if q is None:
             T, d = Tk, dk
-        elif k.dtype != q.dtype or Tk != T or dk != d:
+        elif k.dtype != dtype or Tk != T or dk != d:
             raise ValueError("q and k must agree in type, tokens and head dim")
-    return (k if q is None else q), T, H, Hk, d, qs, ks
+    return dev, dtype, T, H, Hk, d, qs, ks
 
 
 def csa_qk_norm_rope(q, k, inv_freq, wq=None, wk=None, eps=1e-6, pos=None, t0=0, rot_start=0, rot_style=ROPE_HALVES,
@@ -555,22 +584,22 @@ def csa_qk_norm_rope(q, k, inv_freq, wq=None, wk=None, eps=1e-6, pos=None, t0=0,
     the CPU (None: no rotation), turning channels rot_start .. rot_start + rot.
     pos [T] int64 positions on the device, or None: t0, t0 + 1, ...
     Returns (yq, yk) of out_dtype (default: the inputs' type)."""
-    x, T, H, Hk, d, qs, ks = _qk_sides(q, k)
-    ot = x.dtype if out_dtype is None else out_dtype
-    _weight(wq, d, "wq"), _weight(wk, d, "wk"), _vector(pos, T, torch.int64, "pos")
+    dev, dtype, T, H, Hk, d, qs, ks = _qk_sides(q, k)
+    ot = dtype if out_dtype is None else out_dtype
+    wqp, wkp = _vector(wq, d, torch.float32, "wq", dev), _vector(wk, d, torch.float32, "wk", dev)
+    pp = _vector(pos, T, torch.int64, "pos", dev)
     fp, rot = _freq(inv_freq)
     if ot not in _ODTYPE:
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
     if q is not None:
-        yq = _like(q, ot) if yq is None else _given(yq, ot, q.shape, "yq")
+        yq = _like(q, ot) if yq is None else _given(yq, ot, q.shape, "yq", dev)
     if k is not None:
-        yk = _like(k, ot) if yk is None else _given(yk, ot, k.shape, "yk")
+        yk = _like(k, ot) if yk is None else _given(yk, ot, k.shape, "yk", dev)
     if q is None and yq is not None or k is None and yk is not None:
         raise ValueError("an output without its input")
-    dev = _here(q, k, wq, wk, pos, yq, yk)
-    _check(lib().csa_qk_norm_rope(_ptr(q), qs, _ptr(k), ks, _ptr(wq), _ptr(wk), eps, _ptr(pos), t0, fp, rot_start, rot,
-                                  rot_style, T, H, Hk, d, _ODTYPE[x.dtype], _ptr(yq), _ptr(yk), _ODTYPE[ot],
-                                  _stream(dev)), "csa_qk_norm_rope")
+    _check(lib().csa_qk_norm_rope(_ptr(q), qs, _ptr(k), ks, wqp, wkp, eps, pp, t0, fp, rot_start, rot, rot_style, T, H,
+                                  Hk, d, _ODTYPE[dtype], _ptr(yq), _ptr(yk), _ODTYPE[ot], _stream(dev)),
+           "csa_qk_norm_rope")
     return yq, yk
 
 
@@ -579,51 +608,55 @@ def csa_qk_norm_rope_backward(q, k, dyq, dyk, inv_freq, wq=None, wk=None, eps=1e
     """Gradients of csa_qk_norm_rope from dyq/dyk (the types and shapes of yq/yk):
     dq/dk of q's type (given ones may be views of a packed gradient), dwq/dwk [d]
     f32.  Returns (dq, dk, dwq, dwk, workspace), None where there is no input."""
-    x, T, H, Hk, d, qs, ks = _qk_sides(q, k)
-    _weight(wq, d, "wq"), _weight(wk, d, "wk"), _vector(pos, T, torch.int64, "pos")
+    dev, dtype, T, H, Hk, d, qs, ks = _qk_sides(q, k)
+    wqp, wkp = _vector(wq, d, torch.float32, "wq", dev), _vector(wk, d, torch.float32, "wk", dev)
+    pp = _vector(pos, T, torch.int64, "pos", dev)
     fp, rot = _freq(inv_freq)
     dy = dyq if q is not None else dyk
     if dy is None or dy.dtype not in _ODTYPE:
         raise TypeError("the gradients must be torch.bfloat16 or torch.float32")
     yt = dy.dtype
     sides = []
-    for s, dy, dx, w, dw, heads, n in ((q, dyq, dq, wq, dwq, H, "q"), (k, dyk, dk, wk, dwk, Hk, "k")):
-        if s is None:
+    for x, dy, dx, w, dw, heads, n in ((q, dyq, dq, wq, dwq, H, "q"), (k, dyk, dk, wk, dwk, Hk, "k")):
+        if x is None:
             if dy is not None or dx is not None or dw is not None:
                 raise ValueError("gradients of %s without %s" % (n, n))
-            sides.append((None, 0, None))
+            sides.append((None, 0, None, None))
             continue
         shape = (T, heads, d)
-        _given(dy, yt, shape, "dy")
+        _given(dy, yt, shape, "dy", dev)
         if dx is None:
-            dx, stride = _like(s, x.dtype), heads * d
+            dx, stride = _like(x, dtype), heads * d
         else:
-            stride, *got = _rows(dx, (x.dtype,), "dx")
+            stride, *got = _rows(dx, (dtype,), "dx", dev)
             if tuple(got) != shape:
                 raise ValueError("d%s must have shape %s" % (n, shape))
-        if w is not None:
-            dw = torch.empty_like(w) if dw is None else _weight(dw, d, "dw")
-        elif dw is not None:
-            raise ValueError("dw%s without w%s" % (n, n))
-        sides.append((dx, stride, dw))
-    (dq, dqs, dwq), (dk, dks, dwk) = sides
+        if w is None:
+            if dw is not None:
+                raise ValueError("dw%s without w%s" % (n, n))
+            sides.append((dx, stride, None, None))
+        else:
+            dw = torch.empty_like(w) if dw is None else dw
+            sides.append((dx, stride, dw, _vector(dw, d, torch.float32, "dw", dev)))
+    (dq, dqs, dwq, dwqp), (dk, dks, dwk, dwkp) = sides
     L = lib()
-    dev = _here(q, k, wq, wk, pos, dyq, dyk, dq, dk, dwq, dwk, workspace)
-    ws = _scratch(workspace, x.device, lambda: L.csa_qk_norm_rope_backward_workspace_bytes(T, H, Hk, d))
-    _check(L.csa_qk_norm_rope_backward(_ptr(q), qs, _ptr(k), ks, _ptr(wq) if H else None, _ptr(wk) if Hk else None,
-                                       eps, _ptr(pos), t0, fp, rot_start, rot, rot_style, _ptr(dyq), _ptr(dyk), T, H,
-                                       Hk, d, _ODTYPE[x.dtype], _ODTYPE[yt], _ptr(dq), dqs, _ptr(dk), dks, _ptr(dwq),
-                                       _ptr(dwk), _ptr(ws), ws.numel(), _stream(dev)), "csa_qk_norm_rope_backward")
+    ws = _scratch(workspace, dev, lambda: L.csa_qk_norm_rope_backward_workspace_bytes(T, H, Hk, d))
+    _check(L.csa_qk_norm_rope_backward(_ptr(q), qs, _ptr(k), ks, wqp if H else None, wkp if Hk else None, eps, pp, t0,
+                                       fp, rot_start, rot, rot_style, _ptr(dyq), _ptr(dyk), T, H, Hk, d,
+                                       _ODTYPE[dtype], _ODTYPE[yt], _ptr(dq), dqs, _ptr(dk), dks, dwqp, dwkp,
+                                       ws.data_ptr(), ws.numel(), _stream(dev)), "csa_qk_norm_rope_backward")
     return dq, dk, dwq, dwk, ws
 
 
-def _paged(Kpages, Vpages, block_table):
+_BF16 = (torch.bfloat16,)
+
+
+def _paged(Kpages, Vpages, dev):
     """(pages, key heads, rows a page, d) of a paged cache."""
-    _dev(Kpages, torch.bfloat16, "Kpages", 4), _dev(Vpages, torch.bfloat16, "Vpages", 4)
-    _dev(block_table, torch.int32, "block_table", 2)
-    if Kpages.shape != Vpages.shape:
+    shape = _dense(Kpages, torch.bfloat16, 4, "Kpages", dev)
+    if _dense(Vpages, torch.bfloat16, 4, "Vpages", dev) != shape:
         raise ValueError("Kpages and Vpages must have the same shape")
-    return Kpages.shape
+    return shape
 
 
 def csa_paged_append(k, v, Kpages, Vpages, block_table, seq, pos, inv_freq, slot=None, wk=None, eps=1e-6, rot_start=0,
@@ -634,20 +667,22 @@ def csa_paged_append(k, v, Kpages, Vpages, block_table, seq, pos, inv_freq, slot
     [B,max_pages] int32; seq [T] int32; pos, slot [T] int64 on the device (slot
     None: pos; a negative slot skips its token).  Returns the workspace, whose
     status word reports numbers outside their tables."""
-    n_pages, Hk, page, d = _paged(Kpages, Vpages, block_table)
-    ks, T, kh, kd = _rows(k, (torch.bfloat16,), "k")
-    vs, Tv, vh, vd = _rows(v, (torch.bfloat16,), "v")
+    dev = _device(k, "k")
+    n_pages, Hk, page, d = _paged(Kpages, Vpages, dev)
+    B, max_pages = _dense(block_table, torch.int32, 2, "block_table", dev)
+    ks, T, kh, kd = _rows(k, _BF16, "k", dev)
+    vs, Tv, vh, vd = _rows(v, _BF16, "v", dev)
     if Tv != T or kh != Hk or vh != Hk or kd != d or vd != d:
         raise ValueError("k and v must be [T, %d, %d]" % (Hk, d))
-    _vector(seq, T, torch.int32, "seq"), _vector(pos, T, torch.int64, "pos"), _vector(slot, T, torch.int64, "slot")
-    _weight(wk, d, "wk")
+    wp = _vector(wk, d, torch.float32, "wk", dev)
+    pp, sp = _vector(pos, T, torch.int64, "pos", dev), _vector(slot, T, torch.int64, "slot", dev)
+    bp = _vector(seq, T, torch.int32, "seq", dev)
     fp, rot = _freq(inv_freq)
-    dev = _here(k, v, Kpages, Vpages, block_table, seq, pos, slot, wk, workspace)
-    ws = _scratch(workspace, k.device, lambda: 256)
-    _check(lib().csa_paged_append(_ptr(k), ks, _ptr(v), vs, _ptr(wk), eps, _ptr(pos), _ptr(slot), _ptr(seq), fp,
-                                  rot_start, rot, rot_style, _ptr(block_table), T, Hk, d, block_table.shape[0],
-                                  block_table.shape[1], n_pages, page, _ptr(Kpages), _ptr(Vpages), _ptr(ws),
-                                  ws.numel(), _stream(dev)), "csa_paged_append")
+    ws = _scratch(workspace, dev, lambda: 256)
+    _check(lib().csa_paged_append(k.data_ptr(), ks, v.data_ptr(), vs, wp, eps, pp, sp, bp, fp, rot_start, rot,
+                                  rot_style, block_table.data_ptr(), T, Hk, d, B, max_pages, n_pages, page,
+                                  Kpages.data_ptr(), Vpages.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)),
+           "csa_paged_append")
     return ws
 
 
@@ -658,25 +693,25 @@ def csa_tree_attn(q, Kpages, Vpages, block_table, seq_lens, q_start, mask, scale
     b, whose cache rows follow its seq_lens[b] committed ones; mask [R] int64
     (storage of the uint64 bits): the drafted rows of its own sequence that a row
     sees; W >= 0: committed rows s > pos[r] - W only.  Returns (O, lse, workspace)."""
-    n_pages, Hk, page, d = _paged(Kpages, Vpages, block_table)
-    _dev(q, torch.bfloat16, "q", 3)
-    R, H, dq = q.shape
+    dev = _device(q, "q")
+    n_pages, Hk, page, d = _paged(Kpages, Vpages, dev)
+    B, max_pages = _dense(block_table, torch.int32, 2, "block_table", dev)
+    shape = _dense(q, torch.bfloat16, 3, "q", dev)
+    R, H, dq = shape
     if dq != d:
         raise ValueError("q must have head dim %d, got %d" % (d, dq))
-    B, max_pages = block_table.shape
-    _vector(seq_lens, B, torch.int32, "seq_lens"), _vector(q_start, B + 1, torch.int32, "q_start")
-    _vector(mask, R, torch.int64, "mask"), _vector(pos, R, torch.int64, "pos")
+    lp, sp = _vector(seq_lens, B, torch.int32, "seq_lens", dev), _vector(q_start, B + 1, torch.int32, "q_start", dev)
+    mp, pp = _vector(mask, R, torch.int64, "mask", dev), _vector(pos, R, torch.int64, "pos", dev)
     if out_dtype not in _ODTYPE:
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
-    O = _like(q, out_dtype) if O is None else _given(O, out_dtype, q.shape, "O")
+    O = _like(q, out_dtype) if O is None else _given(O, out_dtype, shape, "O", dev)
     if lse is not None:
-        _given(lse, torch.float32, (R, H), "lse")
+        _given(lse, torch.float32, (R, H), "lse", dev)
     elif want_lse:
         lse = q.new_empty((R, H), dtype=torch.float32)
     L = lib()
-    dev = _here(q, Kpages, Vpages, block_table, seq_lens, q_start, mask, pos, O, lse, workspace)
-    ws = _scratch(workspace, q.device, lambda: L.csa_tree_attn_workspace_bytes(B, R, H, Hk, d, page, max_pages))
-    _check(L.csa_tree_attn(_ptr(q), _ptr(Kpages), _ptr(Vpages), _ptr(block_table), _ptr(seq_lens), _ptr(q_start),
-                           _ptr(mask), _ptr(pos), R, B, H, Hk, d, page, n_pages, max_pages, W, scale, _ptr(O),
-                           _ODTYPE[out_dtype], _ptr(lse), _ptr(ws), ws.numel(), _stream(dev)), "csa_tree_attn")
+    ws = _scratch(workspace, dev, lambda: L.csa_tree_attn_workspace_bytes(B, R, H, Hk, d, page, max_pages))
+    _check(L.csa_tree_attn(q.data_ptr(), Kpages.data_ptr(), Vpages.data_ptr(), block_table.data_ptr(), lp, sp, mp, pp,
+                           R, B, H, Hk, d, page, n_pages, max_pages, W, scale, O.data_ptr(), _ODTYPE[out_dtype],
+                           _ptr(lse), ws.data_ptr(), ws.numel(), _stream(dev)), "csa_tree_attn")
     return O, lse, ws
