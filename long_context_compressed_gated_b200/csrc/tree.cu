@@ -39,10 +39,10 @@
 // product, since 0 * NaN would not be 0.
 //
 // Bound and measured (without the host): one token of 16 sequences of 64 k .. 131 k rows, 64
-// heads of 128 on one key head (807 MB): HBM, 140 us, 5.8 TB/s (6.3 while streaming).  Trees of
+// heads of 128 on one key head (807 MB): HBM, 139 us, 5.8 TB/s (6.3 while streaming).  Trees of
 // 8 .. 16 nodes over 21 k .. 33 k rows, the same heads: the softmax of 128 x 128 logits, 1024
-// clocks of the SFU at least, beside 1024 clocks of products; 2.0 us for a pair of row tiles,
-// 166 us (190 under the power cap), 0.95 PFLOP/s.  32 heads of 64 on 8 key heads, window 4096:
+// clocks of the SFU at least, beside 1024 clocks of products; 1.9 us for a pair of row tiles,
+// 165 us (186 under the power cap), 0.96 PFLOP/s.  32 heads of 64 on 8 key heads, window 4096:
 // the chain from S over the softmax to PV, 1.0 us a tile, and 3 .. 4 us to change segments; 64 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // raw logits of the row, read in two halves and, but for the first, again for the weights:
           // the loop's code stays small (the warps of a quarter of the SM are in different places
           // of it and wait for instructions otherwise), and half a row fits the 168 registers of
-          // a thread.  The whole row in registers took 200 us for drafted trees (190 now)
+          // a thread.  The whole row in registers took 201 us for drafted trees (187 now)
           uint32_t v[64];
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
