@@ -399,3 +399,73 @@ def test_verification_step(csa, H, Hk, d, page, W):
     assert ((yq.cpu().double() - q).abs() <= qb).all()
     x["q"] = yq.cpu()
     check(x, O, lse, W=W)
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+def test_verification_step_is_its_three_calls(csa, out):
+    """Rows of a wider projection, eager and captured, bit for bit as the three functions."""
+    from long_context_compressed_gated_b200.speculative import tree_verify_step
+    H, Hk, d, page, lens, nodes = 12, 3, 64, 16, [200, 31], [5, 9]
+    x = make(lens, nodes, H, Hk, d, page, seed=40)
+    c = {k: v.cuda() for k, v in x.items()}
+    R, width = x["q"].shape[0], (H + 2 * Hk) * d
+    g = torch.Generator().manual_seed(41)
+    qkv = torch.randn(R, width + 64, generator=g).to(BF).cuda()[:, :width]
+    seq = torch.tensor([b for b in range(2) for _ in range(nodes[b])], dtype=torch.int32).cuda()
+    slot = torch.tensor([lens[b] + i for b in range(2) for i in range(nodes[b])]).cuda()
+    f, w = csa.rope_inv_freq(32), torch.ones(d, device="cuda")
+    v = qkv.view(R, H + 2 * Hk, d)
+    Kp, Vp = c["Kp"].clone(), c["Vp"].clone()
+    q, _ = csa.csa_qk_norm_rope(v[:, :H], None, f, wq=w, pos=c["pos"], eps=1e-5)
+    csa.csa_paged_append(v[:, H:H + Hk], v[:, H + Hk:], Kp, Vp, c["table"], seq, c["pos"], f, slot=slot, wk=w, eps=1e-5)
+    want, wl, _ = csa.csa_tree_attn(q, Kp, Vp, c["table"], c["lens"], c["start"], c["mask"], 0.2, W=150, pos=c["pos"],
+                                    out_dtype=out)
+    lse, ws = torch.empty(R, H, device="cuda"), torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")
+
+    def step(O=None, **kw):
+        return tree_verify_step(qkv, H, Hk, c["Kp"], c["Vp"], c["table"], c["lens"], c["start"], c["mask"], seq, slot,
+                                c["pos"], f, 0.2, wq=w, wk=w, eps=1e-5, W=150, O=O, out_dtype=out, **kw)
+
+    def same(O):
+        bits = lambda t: t.view(torch.int16)
+        return torch.equal(O, want) and torch.equal(bits(c["Kp"]), bits(Kp)) and torch.equal(bits(c["Vp"]), bits(Vp))
+
+    assert same(step(lse=lse)) and torch.equal(lse, wl)
+    O = torch.empty_like(want)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(O=O, workspace=ws)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            step(O=O, workspace=ws)
+    torch.cuda.synchronize()
+    O.zero_(), c["Kp"].copy_(x["Kp"]), c["Vp"].copy_(x["Vp"])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert same(O) and csa.csa_check_status(ws) == 0
+    none = [t[:0] for t in (qkv, c["mask"], seq, slot, c["pos"])]
+    e = tree_verify_step(none[0], H, Hk, c["Kp"], c["Vp"], c["table"], c["lens"], c["start"] * 0, none[1], none[2],
+                         none[3], none[4], f, 0.2)
+    assert e.shape == (0, H, d)
+
+
+def test_verification_step_refuses(csa):
+    from long_context_compressed_gated_b200.speculative import tree_verify_step
+    x = make([20], [2], 4, 2, 64, 16, seed=42)
+    c = {k: v.cuda() for k, v in x.items()}
+    seq, slot = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.tensor([20, 21]).cuda()
+    good = dict(qkv=torch.zeros(2, 8 * 64, dtype=BF, device="cuda"), H=4, Hk=2, Kpages=c["Kp"], Vpages=c["Vp"],
+                block_table=c["table"], seq_lens=c["lens"], q_start=c["start"], mask=c["mask"], seq=seq, slot=slot,
+                pos=c["pos"], inv_freq=csa.rope_inv_freq(64), scale=0.1)
+    tree_verify_step(**good)
+    for change, error in ((dict(H=5), ValueError), (dict(Hk=1), ValueError), (dict(qkv=good["qkv"].float()), TypeError),
+                          (dict(qkv=good["qkv"].cpu()), TypeError), (dict(qkv=good["qkv"][0]), ValueError),
+                          (dict(qkv=good["qkv"].t().contiguous().t()), ValueError), (dict(pos=None), ValueError),
+                          (dict(slot=slot[:1]), ValueError), (dict(seq=slot), TypeError),
+                          (dict(mask=c["mask"].cpu()), TypeError), (dict(out_dtype=torch.float16), TypeError),
+                          (dict(O=torch.zeros(2, 4, 32, dtype=BF, device="cuda")), ValueError),
+                          (dict(lse=torch.zeros(2, 4, dtype=BF, device="cuda")), TypeError),
+                          (dict(workspace=torch.zeros(256, dtype=torch.uint8, device="cuda")), csa.CsaError),
+                          (dict(scale=0.0), csa.CsaError), (dict(wq=torch.zeros(32, device="cuda")), ValueError)):
+        with pytest.raises(error):
+            tree_verify_step(**dict(good, **change))

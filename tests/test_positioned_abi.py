@@ -118,3 +118,6 @@ def test_binding_refuses_host_tensors():
         csa.csa_qk_norm_rope(None, None, csa.rope_inv_freq(64))
     with pytest.raises(TypeError):
         csa.csa_paged_append(q, q, q, q, q, q, q, None)
+    from long_context_compressed_gated_b200.speculative import tree_verify_step
+    with pytest.raises(TypeError):
+        tree_verify_step(q[0], 2, 1, q, q, q, q, q, q, q, q, q, None, 1.0)
