@@ -636,8 +636,11 @@ def csa_qk_norm_rope_backward(q, k, dyq, dyk, inv_freq, wq=None, wk=None, eps=1e
                 raise ValueError("dw%s without w%s" % (n, n))
             sides.append((dx, stride, None, None))
         else:
-            dw = torch.empty_like(w) if dw is None else dw
-            sides.append((dx, stride, dw, _vector(dw, d, torch.float32, "dw", dev)))
+            if dw is None:
+                dw = torch.empty_like(w)
+                sides.append((dx, stride, dw, dw.data_ptr()))
+            else:
+                sides.append((dx, stride, dw, _vector(dw, d, torch.float32, "dw", dev)))
     (dq, dqs, dwq, dwqp), (dk, dks, dwk, dwkp) = sides
     L = lib()
     ws = _scratch(workspace, dev, lambda: L.csa_qk_norm_rope_backward_workspace_bytes(T, H, Hk, d))
