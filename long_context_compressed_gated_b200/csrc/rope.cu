@@ -15,6 +15,7 @@
 
 #include "checks.cuh"
 #include "rope.cuh"
+#include "sm100.cuh"
 
 namespace csa {
 
@@ -43,13 +44,15 @@ namespace {
 
 constexpr int kThreads = 256;      // forward
 constexpr int kAhead = 4;          // rows of a group loaded before the first is used
-// Backward: the bytes in flight are limited by its registers.  Blocks of 128 threads per SM
-// and rows of a group ahead, by types; 600 MB of 65 heads of 128, with the sum of dw (the
-// bytes alone take 92 us): bf16 five and two 117, four and three 131, six and two 142 us;
-// fp32 four and three 106, five and two 134, three and four 113; mixed four and three 112.
+// Backward: blocks per SM and rows of a group on their way, by element sizes.  600 MB of 65
+// heads of 128 with the sum of dw (the bytes alone take 92 us): bf16 five and three 101 us (two
+// 106, four 102; six and three 117); fp32 four and four 97 (three 105, five blocks 124); fp32
+// gradients of bf16 four and four 95 (five blocks 106); bf16 gradients of fp32 five and five
+// 106 (four ahead 115, four blocks 114).
 constexpr int kBwdThreads = 128;
+constexpr int bwd_blocks_per_sm(int bytes_y) { return bytes_y == 4 ? 4 : 5; }
+constexpr int bwd_ahead(int bytes_x, int bytes_y) { return bytes_y == 4 ? 4 : bytes_x == 4 ? 5 : 3; }
 constexpr bool bwd_wide(int bytes_x, int bytes_y) { return bytes_x + bytes_y > 4; }
-constexpr int bwd_blocks_per_sm(bool wide) { return wide ? 4 : 5; }
 // Most heads of one token that share a set of coefficients: fewer sets with 16, shorter pieces
 // of memory with 8.  Forward, 600 MB: bf16 outputs 102 against 115 us with 8, fp32 outputs
 // 98 against 94; backward: bf16 118 against 128, with an fp32 side 106 against 100.
@@ -73,6 +76,20 @@ struct RopeArgs {
   int64_t T;
   float* dw_part;  // backward: [blocks of both sides][d] partial weight gradients
 };
+
+// A lane's piece of a row on its way into shared memory.  L1: through the first-level cache
+// (two pieces of 16 bytes share each 32-byte sector of an fp32 row: 97 us against 158).
+template <bool L1>
+__device__ __forceinline__ void copy16(uint4* to, const uint4* from) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+  if (L1) asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+  else asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+}
+// The lane's piece of a row in shared memory, as load8 gives it.
+__device__ __forceinline__ void take(Raw8b& r, const uint4* p) { r.v = p[0]; }
+__device__ __forceinline__ void take(Raw8f& r, const uint4* p) {
+  r.a = *reinterpret_cast<const float4*>(p), r.b = *reinterpret_cast<const float4*>(p + kBwdThreads);
+}
 
 template <int D, typename TX, typename TY, int STYLE>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
@@ -122,80 +139,124 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
 // Backward.  A block's groups take its side's units in turn (block i of the side
 // the units i * GROUPS .., i * GROUPS + blocks * GROUPS .., ...), keep their share
 // of dw in registers, and the block adds its groups' shares in order: one partial
-// row per block, summed in order by norm_rope_dw_kernel (no atomics).
+// row per block, summed in order by norm_rope_dw_kernel (no atomics).  Rows wait in
+// shared memory, not in registers: the bytes in flight are what bounds it (rows in
+// registers: 117 us where this takes 101, 16384 tokens of 65 heads 149 and 136).
 template <int D, typename TX, typename TY, int STYLE>
-__global__ void __launch_bounds__(kBwdThreads, bwd_blocks_per_sm(bwd_wide(sizeof(TX), sizeof(TY))))
+__global__ void __launch_bounds__(kBwdThreads, bwd_blocks_per_sm(sizeof(TY)))
     norm_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int LPR = D / 8, GROUPS = kBwdThreads / LPR, kBwdAhead = bwd_wide(sizeof(TX), sizeof(TY)) ? 3 : 2;
+  constexpr int LPR = D / 8, GROUPS = kBwdThreads / LPR;
+  constexpr int kAheadRows = bwd_ahead(sizeof(TX), sizeof(TY));
+  constexpr int PX = sizeof(TX) / 2, PY = sizeof(TY) / 2;   // 16-byte pieces of a lane's eight channels
   __shared__ uint64_t s_turn[kRopeMaxPairs];
   __shared__ float s_dw[GROUPS * D];
+  __shared__ uint4 s_row[kAheadRows + 1][PX + PY][kBwdThreads];
   stage_turns(a.p, s_turn);
   const bool keys = (int64_t)blockIdx.x >= a.side[0].blocks;
   const RopeSide& sd = a.side[keys];
   const int64_t block = (int64_t)blockIdx.x - (keys ? a.side[0].blocks : 0);
   const uint32_t mask = group_mask<D>();
   const RopeLane rl = rope_lane<D, STYLE>(a.p);
-  using RawX = typename RawOf<TX>::type;
-  using RawY = typename RawOf<TY>::type;
   float w[8], dw[8], one[8];
   load_weights(sd.w, rl.l, w);
 #pragma unroll
   for (int j = 0; j < 8; ++j) dw[j] = 0.f, one[j] = 1.f;
   const bool norm = sd.w != nullptr;
-  const int64_t units = a.T * sd.chunks;
-  for (int64_t unit = block * GROUPS + threadIdx.x / LPR; unit < units; unit += sd.blocks * GROUPS) {
-    const int64_t t = unit / sd.chunks;
-    const int h0 = (int)(unit % sd.chunks) * sd.chunk;
-    const int n = sd.heads - h0 < sd.chunk ? sd.heads - h0 : sd.chunk;
-    const TX* x = static_cast<const TX*>(sd.x) + t * sd.x_stride + (int64_t)h0 * D + 8 * rl.l;
-    const TY* dy = static_cast<const TY*>(sd.dy) + (t * sd.heads + h0) * D + 8 * rl.l;
-    TX* dx = static_cast<TX*>(sd.dx) + t * sd.dx_stride + (int64_t)h0 * D + 8 * rl.l;
-    RawX rx[kBwdAhead];
-    RawY ry[kBwdAhead];
+  const int64_t step = sd.blocks * GROUPS, first = block * GROUPS + threadIdx.x / LPR;
+  const int64_t step_t = step / sd.chunks;
+  const int step_c = (int)(step - step_t * sd.chunks);
+  // a place in the group's units: token, chunk of heads
+  struct Place {
+    int64_t t;
+    int c;
+  };
+  auto next = [&](Place& p) {
+    p.t += step_t, p.c += step_c;
+    if (p.c >= sd.chunks) p.c -= sd.chunks, ++p.t;
+  };
+  auto size = [&](const Place& p) {
+    const int left = sd.heads - p.c * sd.chunk;
+    return left < sd.chunk ? left : sd.chunk;
+  };
+  Place at;
+  at.t = first / sd.chunks, at.c = (int)(first - at.t * sd.chunks);
+  // The copies run kAheadRows rows ahead, across units: every lane copies, and later reads, its
+  // own pieces, so nobody waits for another.
+  Place ahead = at;
+  int ah = 0, an = 0;
+  const TX* ax = nullptr;
+  const TY* ay = nullptr;
+  auto open = [&]() {
+    if (ahead.t < a.T) {
+      const int h0 = ahead.c * sd.chunk;
+      ax = static_cast<const TX*>(sd.x) + ahead.t * sd.x_stride + (int64_t)h0 * D + 8 * rl.l;
+      ay = static_cast<const TY*>(sd.dy) + (ahead.t * sd.heads + h0) * D + 8 * rl.l;
+      an = size(ahead);
+    }
+    ah = 0;
+  };
+  open();
+  auto fetch = [&](int slot) {
+    if (ahead.t < a.T) {
 #pragma unroll
-    for (int u = 0; u < kBwdAhead; ++u)
-      if (u < n) load8(x + u * D, rx[u]), load8(dy + u * D, ry[u]);
+      for (int i = 0; i < PX; ++i) copy16<(PX > 1)>(&s_row[slot][i][threadIdx.x], reinterpret_cast<const uint4*>(ax) + i);
+#pragma unroll
+      for (int i = 0; i < PY; ++i) copy16<(PY > 1)>(&s_row[slot][PX + i][threadIdx.x], reinterpret_cast<const uint4*>(ay) + i);
+      ax += D, ay += D;
+      if (++ah == an) next(ahead), open();
+    }
+    sm100::cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kAheadRows; ++i) fetch(i);
+  int slot = 0;
+  auto position = [&](const Place& p) { return a.p.pos ? (p.t < a.T ? a.p.pos[p.t] : 0) : a.p.t0 + p.t; };
+  int64_t pos = position(at);
+#pragma unroll 1
+  while (at.t < a.T) {
+    const int n = size(at), h0 = at.c * sd.chunk;
+    TX* dx = static_cast<TX*>(sd.dx) + at.t * sd.dx_stride + (int64_t)h0 * D + 8 * rl.l;
     float A[8], B[8];
     {
       float c[8], s[8];
-      rope_angles<STYLE>(rl, s_turn, a.p.pos ? a.p.pos[t] : a.p.t0 + t, mask, c, s);
+      rope_angles<STYLE>(rl, s_turn, pos, mask, c, s);
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[j] = -s[j];  // the transpose turns back
       rope_coef<STYLE>(rl, c, s, one, one, A, B);
     }
-    for (int h = 0; h < n; h += kBwdAhead) {
+    next(at);
+    pos = position(at);
+#pragma unroll 1
+    for (int h = 0; h < n; ++h) {
+      sm100::cp_async_wait<kAheadRows - 1>();
+      typename RawOf<TX>::type cx;
+      typename RawOf<TY>::type cy;
+      take(cx, &s_row[slot][0][threadIdx.x]);
+      take(cy, &s_row[slot][PX][threadIdx.x]);
+      float f[8], e[8], g[8];
+      unpack8(cx, f);
+      unpack8(cy, e);
+      fetch(slot == 0 ? kAheadRows : slot - 1);  // the place of the row before
+      slot = slot == kAheadRows ? 0 : slot + 1;
+      rope_row<STYLE>(cy, e, 1.f, A, B, rl.partner, mask, g);
+      if (norm) {
+        float q = 0.f, v = 0.f;
 #pragma unroll
-      for (int u = 0; u < kBwdAhead; ++u) {
-        if (h + u >= n) break;
-        const RawX cx = rx[u];
-        const RawY cy = ry[u];
-        if (h + u + kBwdAhead < n) {
-          load8(x + (int64_t)(h + u + kBwdAhead) * D, rx[u]);
-          load8(dy + (int64_t)(h + u + kBwdAhead) * D, ry[u]);
+        for (int j = 0; j < 8; ++j) q = fmaf(f[j], f[j], q), v = fmaf(g[j] * w[j], f[j], v);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) {
+          q += __shfl_xor_sync(mask, q, o);
+          v += __shfl_xor_sync(mask, v, o);
         }
-        float f[8], e[8], g[8];
-        unpack8(cx, f);
-        unpack8(cy, e);
-        rope_row<STYLE>(cy, e, 1.f, A, B, rl.partner, mask, g);
-        if (norm) {
-          float q = 0.f, v = 0.f;
+        const float r = rsqrtf(q * (1.0f / D) + a.p.eps);
+        const float k = v * (1.0f / D) * r * r;  // x k = xh mean(g w xh)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) q = fmaf(f[j], f[j], q), v = fmaf(g[j] * w[j], f[j], v);
-#pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) {
-            q += __shfl_xor_sync(mask, q, o);
-            v += __shfl_xor_sync(mask, v, o);
-          }
-          const float r = rsqrtf(q * (1.0f / D) + a.p.eps);
-          const float k = v * (1.0f / D) * r * r;  // x k = xh mean(g w xh)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            dw[j] = fmaf(g[j], f[j] * r, dw[j]);
-            g[j] = r * fmaf(-f[j], k, g[j] * w[j]);
-          }
+        for (int j = 0; j < 8; ++j) {
+          dw[j] = fmaf(g[j], f[j] * r, dw[j]);
+          g[j] = r * fmaf(-f[j], k, g[j] * w[j]);
         }
-        store8(dx + (int64_t)(h + u) * D, g);
       }
+      store8(dx + (int64_t)h * D, g);
     }
   }
   if (!norm) return;
@@ -243,16 +304,16 @@ int64_t side_units(int64_t T, int heads, int d, bool wide) {
 
 // Blocks of the queries and of the keys in the backward pass: all at once on the GPU, each
 // with its share of the work; each leaves one partial row of dw.
-void bwd_split(int64_t T, int H, int Hk, int d, bool wide, int64_t* blocks) {
+void bwd_split(int64_t T, int H, int Hk, int d, int bytes_x, int bytes_y, int64_t* blocks) {
   const int heads[2] = {H, Hk};
   int64_t need[2] = {0, 0}, work[2] = {0, 0};
   for (int i = 0; i < 2; ++i) {
     if (heads[i] <= 0) continue;
-    const int64_t units = side_units(T, heads[i], d, wide);
+    const int64_t units = side_units(T, heads[i], d, bwd_wide(bytes_x, bytes_y));
     need[i] = ceil_div(units, kBwdThreads / (d / 8));
     work[i] = T * heads[i] + units * kUnitRows;
   }
-  const int64_t most = (int64_t)bwd_blocks_per_sm(wide) * sm_count();
+  const int64_t most = (int64_t)bwd_blocks_per_sm(bytes_y) * sm_count();
   blocks[0] = need[0], blocks[1] = need[1];
   if (need[0] + need[1] <= most) return;
   int64_t k = (int64_t)((double)most * work[1] / (work[0] + work[1]) + 0.5);
@@ -371,8 +432,8 @@ int csa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_s
 size_t csa_qk_norm_rope_backward_workspace_bytes(int64_t T, int H, int Hk, int d) {
   if (T <= 0 || d <= 0) return kWorkspaceHeader;
   int64_t most = 0, blocks[2];
-  for (bool wide : {false, true}) {  // whatever the types
-    bwd_split(T, H, Hk, d, wide, blocks);
+  for (int types = 0; types < 4; ++types) {  // whatever they are
+    bwd_split(T, H, Hk, d, types & 1 ? 4 : 2, types & 2 ? 4 : 2, blocks);
     if (blocks[0] + blocks[1] > most) most = blocks[0] + blocks[1];
   }
   return kWorkspaceHeader + align256((size_t)most * d * 4);
@@ -385,9 +446,9 @@ int csa_qk_norm_rope_backward(const void* q, int64_t q_stride, const void* k, in
                               int64_t dk_stride, float* dwq, float* dwk, void* workspace, size_t workspace_bytes,
                               csa_stream_t stream) {
   RopeArgs a{};
-  const bool wide = bwd_wide(x_dtype == CSA_BF16 ? 2 : 4, y_dtype == CSA_BF16 ? 2 : 4);
+  const int bytes_x = x_dtype == CSA_BF16 ? 2 : 4, bytes_y = y_dtype == CSA_BF16 ? 2 : 4;
   int rc = check_rope(T, H, Hk, d, x_dtype, y_dtype, q, q_stride, k, k_stride, wq, wk, eps, inv_freq, rot_start,
-                      rot_dim, rot_style, wide, a);
+                      rot_dim, rot_style, bwd_wide(bytes_x, bytes_y), a);
   if (rc) return rc;
   if ((rc = check_opt(pos))) return rc;
   if ((H > 0 && wq != nullptr) != (dwq != nullptr) || (Hk > 0 && wk != nullptr) != (dwk != nullptr))
@@ -411,7 +472,7 @@ int csa_qk_norm_rope_backward(const void* q, int64_t q_stride, const void* k, in
   }
   if (H == 0 && Hk == 0) return CSA_OK;
   int64_t blocks[2];
-  bwd_split(T, H, Hk, d, wide, blocks);
+  bwd_split(T, H, Hk, d, bytes_x, bytes_y, blocks);
   for (int i = 0; i < 2; ++i) {
     if (heads[i] == 0) continue;
     if ((rc = check_ptrs(dy[i], dx[i]))) return rc;
