@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_blocks_per_sm(sizeof(TY)))
   __shared__ uint64_t s_turn[kRopeMaxPairs];
   __shared__ float s_dw[GROUPS * D];
   __shared__ uint4 s_row[kAheadRows + 1][PX + PY][kBwdThreads];
+  griddep_launch_dependents();  // the sum of dw is set up while the last blocks run
   stage_turns(a.p, s_turn);
   const bool keys = (int64_t)blockIdx.x >= a.side[0].blocks;
   const RopeSide& sd = a.side[keys];
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(32 * kDwWarps) norm_rope_dw_kernel(const float
   __shared__ float s[kDwWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float sum = 0.f;
-#pragma unroll 8
+#pragma unroll 12
   for (int64_t i = warp; i < n; i += kDwWarps) sum += p[i * D + c];
   s[warp][lane] = sum;
   __syncthreads();
