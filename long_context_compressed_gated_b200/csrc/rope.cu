@@ -9,8 +9,10 @@
 //
 // Bound: HBM.  Forward reads x and writes y once; backward reads x and dy and
 // writes dx.  A group of d/8 lanes takes one token's chunk of heads, so the
-// rotation's coefficients are built once per chunk; the rows of a chunk are
-// loaded kAhead at a time before any is used, to keep enough bytes in flight.
+// rotation's coefficients are built once per chunk; to keep enough bytes in flight
+// the forward loads kAhead rows before it uses one (32768 tokens of 65 heads of 128,
+// bf16, 1.09 GB: 173 us, 6.3 TB/s), the backward has rows on their way in shared memory
+// (half the tokens, 0.82 GB: 127 us, 6.4 TB/s, then the sum of dw).
 #include <cmath>
 
 #include "checks.cuh"
