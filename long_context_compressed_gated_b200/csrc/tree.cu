@@ -1117,8 +1117,10 @@ bool page_map(CUtensorMap* m, const void* base, int64_t n_pages, int Hk, int pag
 }
 
 // CTAs of a call: one per SM, fewer when even the longest sequences that the
-// tables can hold give less than kMinShare key tiles each.
+// tables can hold give less than kMinShare key tiles each.  Without a page a sequence has
+// no node, or is reported: one CTA looks.
 int tree_ctas(int B, int64_t R, int H, int Hk, int page, int max_pages) {
+  if (max_pages == 0) return 1;
   const int64_t sms = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
   const int64_t nodes = R < kMaxNodes ? R : kMaxNodes;
   const int64_t seqs = B < R ? B : R;  // with a node
@@ -1155,9 +1157,10 @@ using namespace csa;
 
 extern "C" {
 
-// [header][split 2 x int4 per CTA][partial lse][partial O], two slots per CTA
+// [header][split 2 x int4 per CTA][partial lse][partial O], two slots per CTA: for every
+// call that launches one (the header alone where csa_tree_attn refuses or has no rows)
 size_t csa_tree_attn_workspace_bytes(int B, int64_t R, int H, int Hk, int d, int page, int max_pages) {
-  if (B <= 0 || R <= 0 || H <= 0 || Hk <= 0 || H < Hk || page <= 0 || max_pages <= 0) return kWorkspaceHeader;
+  if (B <= 0 || R <= 0 || H <= 0 || Hk <= 0 || H < Hk || page <= 0 || max_pages < 0) return kWorkspaceHeader;
   const int ctas = tree_ctas(B, R, H, Hk, page, max_pages);
   const size_t rows = ctas > 1 ? (size_t)2 * ctas * part_rows(R, H, Hk) : 0;
   return kWorkspaceHeader + align256((size_t)ctas * 32) + align256(rows * 4) + align256(rows * d * 4);
