@@ -173,13 +173,15 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b, bool tell) {
   q.r0 = a.q_start[b];
   const int r1 = a.q_start[b + 1];
   q.L = a.lens[b];
-  q.n = r1 - q.r0;
+  q.n = 0;
   q.S = 0;
   q.lo = 0;
-  if (q.r0 < 0 || q.n < 0 || r1 > a.R || q.L < 0 || q.n > kMaxNodes ||
-      (int64_t)q.L + q.n > ((int64_t)a.max_pages << a.page_shift)) {
-    if (tell) report(a.status, CSA_ERR_INDEX);
-    q.n = 0;
+  // compared before they are subtracted: the numbers may be anything, their difference may wrap
+  const bool rows = q.r0 >= 0 && r1 >= q.r0 && r1 <= a.R && r1 - q.r0 <= kMaxNodes;
+  if (rows && q.L >= 0 && (int64_t)q.L + (r1 - q.r0) <= ((int64_t)a.max_pages << a.page_shift)) {
+    q.n = r1 - q.r0;
+  } else if (tell) {
+    report(a.status, CSA_ERR_INDEX);
   }
   if (q.n == 0) {
     q.tiles = q.units = 0;

@@ -47,3 +47,21 @@ def test_tree_attention_with_tables_without_pages(csa, nodes):
     assert untouched(whole, need)
     if not nodes:
         assert (O == 7).all()
+
+
+@pytest.mark.parametrize("r0,r1", [(2 ** 31 - 1, -2 ** 31), (2 ** 31 - 3, -2 ** 31 + 20), (5, -2 ** 31), (-2 ** 31, 2 ** 31 - 1),
+                                   (2 ** 31 - 1, 2 ** 31 - 1), (-1, 0), (11, 11)])
+def test_row_numbers_that_wrap_are_reported(csa, r0, r1):
+    """q_start whose difference in 32 bits looks like a few nodes: reported, and the rows of the
+    call, none of which it names, are left."""
+    B, R, H, d, page = 1, 10, 8, 64, 16
+    q = torch.randn(R, H, d, device="cuda").to(BF)
+    pages = torch.randn(6, 2, page, d, device="cuda").to(BF)
+    table = torch.arange(6, dtype=torch.int32, device="cuda").view(B, 6)
+    lens = torch.tensor([40], dtype=torch.int32, device="cuda")
+    mask, pos = (torch.ones(R, dtype=torch.int64, device="cuda") for _ in range(2))
+    start = torch.tensor([r0, r1], dtype=torch.int32, device="cuda")
+    O = torch.full((R, H, d), 7.0, dtype=BF, device="cuda")
+    for W in (-1, 4):
+        _, _, ws = csa.csa_tree_attn(q, pages, pages.clone(), table, lens, start, mask, 0.1, W=W, pos=pos, O=O)
+        assert csa.csa_check_status(ws) == -8 and (O == 7).all()
