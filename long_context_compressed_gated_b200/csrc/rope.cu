@@ -433,7 +433,7 @@ int csa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_s
 }
 
 size_t csa_qk_norm_rope_backward_workspace_bytes(int64_t T, int H, int Hk, int d) {
-  if (T <= 0 || d <= 0) return kWorkspaceHeader;
+  if (T <= 0 || (d != 64 && d != 128)) return kWorkspaceHeader;  // no rows, or a head dim that is refused
   int64_t most = 0, blocks[2];
   for (int types = 0; types < 4; ++types) {  // whatever they are
     bwd_split(T, H, Hk, d, types & 1 ? 4 : 2, types & 2 ? 4 : 2, blocks);

@@ -1162,7 +1162,8 @@ extern "C" {
 // [header][split 2 x int4 per CTA][partial lse][partial O], two slots per CTA: for every
 // call that launches one (the header alone where csa_tree_attn refuses or has no rows)
 size_t csa_tree_attn_workspace_bytes(int B, int64_t R, int H, int Hk, int d, int page, int max_pages) {
-  if (B <= 0 || R <= 0 || H <= 0 || Hk <= 0 || H < Hk || page <= 0 || max_pages < 0) return kWorkspaceHeader;
+  if (B <= 0 || R <= 0 || H <= 0 || Hk <= 0 || H < Hk || (d != 64 && d != 128) || page <= 0 || max_pages < 0)
+    return kWorkspaceHeader;
   const int ctas = tree_ctas(B, R, H, Hk, page, max_pages);
   const size_t rows = ctas > 1 ? (size_t)2 * ctas * part_rows(R, H, Hk) : 0;
   return kWorkspaceHeader + align256((size_t)ctas * 32) + align256(rows * 4) + align256(rows * d * 4);
