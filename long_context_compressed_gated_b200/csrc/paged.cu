@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(const __grid_
       float f[8], o[8];
       unpack8(ck, f);
       const float r = norm ? row_rms<D>(f, a.p.eps, mask) : 1.f;
-      rope_row<STYLE>(ck, f, r, A, B, rl.partner, mask, o);
+      rope_row<STYLE>(ck, f, r, A, B, rl, mask, o);
       store8(a.Kp + at, o);
       *reinterpret_cast<uint4*>(a.Vp + at) = cv.v;
     }

@@ -46,6 +46,9 @@ namespace {
 
 constexpr int kThreads = 256;      // forward
 constexpr int kAhead = 4;          // rows of a group loaded before the first is used
+// Forward blocks per SM, by the input's element size.  600 MB of 65 heads of 128: fp32 three 99 and
+// 105 us (halves, pairs; two, as it comes without a bound, 117 and 121); bf16 four.
+constexpr int fwd_blocks_per_sm(int bytes_x) { return bytes_x == 4 ? 3 : 4; }
 // Backward: blocks per SM and rows of a group on their way, by element sizes.  600 MB of 65
 // heads of 128 with the sum of dw (the bytes alone take 92 us): bf16 five and three 101 us (two
 // 106, four 102; six and three 117); fp32 four and four 97 (three 105, five blocks 124); fp32
@@ -94,7 +97,7 @@ __device__ __forceinline__ void take(Raw8f& r, const uint4* p) {
 }
 
 template <int D, typename TX, typename TY, int STYLE>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, fwd_blocks_per_sm(sizeof(TX))) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
   __shared__ uint64_t s_turn[kRopeMaxPairs];
   stage_turns(a.p, s_turn);
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
       float f[8], o[8];
       unpack8(cur, f);
       const float r = norm ? row_rms<D>(f, a.p.eps, mask) : 1.f;
-      rope_row<STYLE>(cur, f, r, A, B, rl.partner, mask, o);
+      rope_row<STYLE>(cur, f, r, A, B, rl, mask, o);
       if (h + u + kAhead < n) load8(x + (int64_t)(h + u + kAhead) * D, raw[u]);
       store8(y + (int64_t)(h + u) * D, o);
     }
@@ -241,7 +244,7 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_blocks_per_sm(sizeof(TY)))
       unpack8(cy, e);
       fetch(slot == 0 ? kAheadRows : slot - 1);  // the place of the row before
       slot = slot == kAheadRows ? 0 : slot + 1;
-      rope_row<STYLE>(cy, e, 1.f, A, B, rl.partner, mask, g);
+      rope_row<STYLE>(cy, e, 1.f, A, B, rl, mask, g);
       if (norm) {
         float q = 0.f, v = 0.f;
 #pragma unroll

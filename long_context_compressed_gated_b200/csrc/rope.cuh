@@ -200,18 +200,17 @@ __device__ __forceinline__ float row_rms(const float* x, float eps, uint32_t mas
   return rsqrtf(a * (1.0f / D) + eps);
 }
 
-// y = r (x A + x' B) for the lane's eight channels of one row.
+// y = r (x A + x' B) for the lane's eight channels of one row.  Channels that are not turned
+// have no partner (B is 0 there, but 0 times an infinite x' would be NaN).
 template <int STYLE, typename Raw>
 __device__ __forceinline__ void rope_row(const Raw& raw, const float* x, float r, const float* A, const float* B,
-                                         int partner, uint32_t mask, float* y) {
-  if (STYLE == CSA_ROPE_HALVES) {
-    float xp[8];
-    unpack8(shfl8(mask, raw, partner), xp);
+                                         const RopeLane& rl, uint32_t mask, float* y) {
+  float xp[8];
+  if (STYLE == CSA_ROPE_HALVES) unpack8(shfl8(mask, raw, rl.partner), xp);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = r * fmaf(xp[j], B[j], x[j] * A[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = r * fmaf(x[j ^ 1], B[j], x[j] * A[j]);
+  for (int j = 0; j < 8; ++j) {
+    const float xa = x[j] * A[j], xb = STYLE == CSA_ROPE_HALVES ? xp[j] : x[j ^ 1];
+    y[j] = r * (rl.turned ? fmaf(xb, B[j], xa) : xa);
   }
 }
 

@@ -23,3 +23,83 @@ def test_backward_refuses_head_dims_without_a_workspace(csa, d):
     x = torch.zeros(3, 2, d, device="cuda")
     with pytest.raises(csa.CsaError):
         csa.csa_qk_norm_rope_backward(x, None, x, None, None)
+
+
+# ---------------------------------------------------------------- values that are not finite
+
+
+def spoiled(T, heads, d, dtype, seed):
+    """Rows with an infinity or a NaN at every channel in turn."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, heads, d, generator=g).to(dtype)
+    for t in range(T):
+        for h in range(heads):
+            x[t, h, (t * heads + h) % d] = (math.inf, -math.inf, math.nan)[(t + h) % 3]
+    return x
+
+
+def same_kind(got, want):
+    """NaN, +inf, -inf and finite in the same places."""
+    got, want = got.cpu().double(), want.double()
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.isposinf(), want.isposinf()) and torch.equal(got.isneginf(), want.isneginf())
+    return want.isfinite()
+
+
+ROTATIONS = [(64, 0, 0), (64, 0, 1), (64, 16, 0), (64, 16, 1), (128, 48, 0), (128, 48, 1), (128, 128, 1), (128, 128, 0)]
+
+
+@pytest.mark.parametrize("d,rot,style", ROTATIONS)
+@pytest.mark.parametrize("normed", [False, True])
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (F32, F32), (BF, F32)])
+def test_norm_rope_keeps_infinities_where_they_are(csa, d, rot, style, normed, dtype, out):
+    """An infinity or a NaN reaches the channels that the formula takes it to (its pair, and with
+    a norm its row's sum of squares), no other; channels outside the rotation keep n."""
+    T, H, start = 24, 6, d - rot
+    x = spoiled(T, H, d, dtype, d + rot + style)
+    f = csa.rope_inv_freq(rot) if rot else None
+    w = torch.linspace(0.5, 1.5, d) if normed else None
+    y, _ = csa.csa_qk_norm_rope(x.cuda(), None, f, wq=None if w is None else w.cuda(), eps=1e-6, t0=3, rot_start=start,
+                                rot_style=style, out_dtype=out)
+    ang = ref.angles(range(3, 3 + T), f if rot else [])
+    want = ref.norm_rope(x, w, 1e-6, ang, start, style)
+    ok = same_kind(y, want)
+    xf = torch.where(x.isfinite(), x.double(), torch.zeros((), dtype=torch.float64))
+    bound = ref.norm_rope_bound(xf, w, 1e-6, ang, start, style, out)
+    err = (y.cpu().double() - want).abs()
+    assert (err[ok] <= bound[ok]).all()
+    if not normed:   # the untouched channels are the input's
+        a, b = y.cpu()[..., :start], x[..., :start].to(out)
+        assert torch.equal(a.nan_to_num(9, 8, 7), b.nan_to_num(9, 8, 7))
+
+
+@pytest.mark.parametrize("d,rot,style", ROTATIONS)
+def test_backward_keeps_infinities_where_they_are(csa, d, rot, style):
+    """Without a norm the gradient is the rotation's transpose of dy."""
+    T, H, start = 24, 6, d - rot
+    dy = spoiled(T, H, d, F32, d + rot + style)
+    x = torch.randn(T, H, d)
+    f = csa.rope_inv_freq(rot) if rot else None
+    dq, *_ = csa.csa_qk_norm_rope_backward(x.cuda(), None, dy.cuda(), None, f, t0=3, rot_start=start, rot_style=style)
+    want = ref.rotate(dy.double(), -ref.angles(range(3, 3 + T), f if rot else []), start, style)
+    same_kind(dq, want)
+    a, b = dq.cpu()[..., :start], dy[..., :start]
+    assert torch.equal(a.nan_to_num(9, 8, 7), b.nan_to_num(9, 8, 7))
+
+
+@pytest.mark.parametrize("d,rot,style", ROTATIONS)
+def test_append_keeps_infinities_where_they_are(csa, d, rot, style):
+    T, Hk, start, page = 32, 6, d - rot, 16
+    x = spoiled(T, Hk, d, BF, d + rot + style)
+    f = csa.rope_inv_freq(rot) if rot else None
+    Kp, Vp = (torch.zeros(2, Hk, page, d, dtype=BF, device="cuda") for _ in range(2))
+    table = torch.tensor([[1, 0]], dtype=torch.int32)
+    pos = torch.arange(3, 3 + T)
+    csa.csa_paged_append(x.cuda(), x.cuda(), Kp, Vp, table.cuda(), torch.zeros(T, dtype=torch.int32, device="cuda"),
+                         pos.cuda(), f, slot=(pos - 3).cuda(), rot_start=start, rot_style=style)
+    k = ref.paged_rows(Kp.cpu(), table, 0, T)
+    want = ref.rotate(x.double(), ref.angles(pos, f if rot else []), start, style)
+    same_kind(k, want)
+    a, b = k[..., :start], x[..., :start]
+    assert torch.equal(a.nan_to_num(9, 8, 7), b.nan_to_num(9, 8, 7))
+    assert torch.equal(ref.paged_rows(Vp.cpu(), table, 0, T).view(torch.int16), x.view(torch.int16))
