@@ -280,6 +280,24 @@ __device__ __forceinline__ uint32_t visible(int off, int lo, int L, uint64_t mas
   return w;
 }
 
+// The drafted rows of a sequence that some node sees: each lane loads two nodes' masks, their OR
+// over the warp is formed where it is needed.
+__device__ __forceinline__ uint64_t lane_masks(const TreeArgs& a, const Segment& s, int lane) {
+  return (lane < s.n ? a.mask[s.r0 + lane] : 0) | (lane + 32 < s.n ? a.mask[s.r0 + 32 + lane] : 0);
+}
+__device__ __forceinline__ uint64_t seen_drafts(uint64_t lane_masks, int n) {
+  return ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(lane_masks >> 32)) << 32 |
+          __reduce_or_sync(0xffffffffu, (uint32_t)lane_masks)) &
+         (n < 64 ? (1ull << n) - 1 : ~0ull);
+}
+// Whether some node sees one of the rows key .. key + rows - 1 (rows at most 128).
+__device__ __forceinline__ bool box_seen(int key, int rows, int lo, int L, uint64_t drafts) {
+  if ((key > lo ? key : lo) < (key + rows < L ? key + rows : L)) return true;
+  const int from = key > L ? key - L : 0, end = key + rows - L;
+  return end > from && from < kMaxNodes &&
+         (drafts >> from & (end - from < 64 ? (1ull << (end - from)) - 1 : ~0ull)) != 0;
+}
+
 // The rest of a bounded wait, out of line: the waits' code stays small.
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* aborted, int* status) {
   const long long start = clock64();
@@ -393,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto entry = [&](int p) { return p <= last_page ? table[p] : -1; };
     int from = (s.t0 * kTile) >> a.page_shift;
     int now = entry(from + lane), next = entry(from + 32 + lane);
+    const uint64_t masks = lane_masks(a, s, lane);
     bool hold = n == 0;
 #pragma unroll 1
     for (int i = loader; i < 2 * nt; i += 2) {
@@ -418,7 +437,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         next = entry(from + 32 + lane);
       }
       int page = __shfl_sync(0xffffffffu, now, ((key >> a.page_shift) - from) & 31);
-      const bool need = lane < boxes && key + box_rows > lo && key < S;
+      // boxes without a row that some node sees are left out, their page numbers unused
+      bool need = lane < boxes && key + box_rows > lo;
+      if (key0 + kTile > s.L) need = box_seen(key, box_rows, lo, s.L, seen_drafts(masks, s.n)) && lane < boxes;
       if (need && (page < 0 || page >= a.n_pages)) {
         report(a.status, CSA_ERR_INDEX);
         page = a.n_pages > 0 ? (int)a.n_pages : 1;  // outside the map: zeros
@@ -618,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // tiles [whole0, whole1) of the segment have no hidden row
       const int whole0 = uniform((s.lo + kTile - 1) / kTile) - t0, whole1 = uniform(s.L / kTile) - t0;
       // drafted rows that some node sees (used, and waited for, at the first tile with hidden rows)
-      const uint64_t seen_by = (lane < s.n ? a.mask[s.r0 + lane] : 0) | (lane + 32 < s.n ? a.mask[s.r0 + 32 + lane] : 0);
+      const uint64_t masks = lane_masks(a, s, lane);
       if (!wait(&q_full[0], (uint32_t)(n & 1)) || (dual && !wait(&q_full[1], q1_phase))) break;
       if (dual) q1_phase ^= 1;
       int ks = 0, vs = 0;      // stages of the K tile of the S to issue and of the V tile of the PV
@@ -652,10 +673,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Rows that no node sees hold anything (or were not fetched).  Sixteen keys are one
             // step of the product: steps without a visible row are left out, the hidden rows of
             // the others zeroed.
-            const uint64_t any = ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(seen_by >> 32)) << 32 |
-                                  __reduce_or_sync(0xffffffffu, (uint32_t)seen_by)) &
-                                 (s.n < 64 ? (1ull << s.n) - 1 : ~0ull);
-            const uint32_t seen = visible((t0 + t) * kTile + 16 * (lane & 7), s.lo, s.L, any) & 0xFFFFu;
+            const uint32_t seen =
+                visible((t0 + t) * kTile + 16 * (lane & 7), s.lo, s.L, seen_drafts(masks, s.n)) & 0xFFFFu;
             steps = __ballot_sync(0xffffffffu, seen != 0) & 0xFFu;
             if (steps == 0) steps = 1;  // (a segment without any visible row still writes its output)
             uint32_t mend = __ballot_sync(0xffffffffu, seen != 0xFFFFu) & steps;

@@ -5,6 +5,8 @@ import math
 import pytest
 import torch
 
+from tests.test_gpu_tree import call, check, make
+
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
 
@@ -65,3 +67,42 @@ def test_row_numbers_that_wrap_are_reported(csa, r0, r1):
     for W in (-1, 4):
         _, _, ws = csa.csa_tree_attn(q, pages, pages.clone(), table, lens, start, mask, 0.1, W=W, pos=pos, O=O)
         assert csa.csa_check_status(ws) == -8 and (O == 7).all()
+
+
+@pytest.mark.parametrize("L,n,real,page", [(62, 8, 2, 64), (62, 8, 0, 64), (0, 9, 1, 16), (15, 64, 17, 16), (127, 33, 1, 128),
+                                           (250, 12, 3, 16), (255, 40, 1, 256)])
+@pytest.mark.parametrize("garbage", [-1, 2 ** 31 - 1])
+def test_pages_behind_the_last_seen_draft_are_not_used(csa, L, n, real, page, garbage):
+    """Padding nodes (mask 0) whose rows would lie in pages that were never taken."""
+    x = make([L, 30], [n, 2], 8, 2, 64, page, seed=L)
+    x["mask"][real:n] = 0
+    x["table"][0, -(-(L + real) // page):] = garbage
+    O, lse, ws = call(csa, x)
+    assert csa.csa_check_status(ws) == 0 and check(x, O, lse).all()
+
+
+@pytest.mark.parametrize("W", [-1, 0, 40])
+@pytest.mark.parametrize("d,page,seed", [(64, 16, 1), (128, 16, 2), (128, 64, 3), (64, 128, 4), (128, 256, 5)])
+def test_pages_that_no_node_sees_are_not_used(csa, W, d, page, seed):
+    """Any masks: a page number is used only if some node sees a row of it."""
+    g = torch.Generator().manual_seed(seed)
+    lens, nodes = [700, 0, 129, 5, 260], [64, 40, 17, 33, 1]
+    x = make(lens, nodes, 8, 2, d, page, seed=seed)
+    r = 0
+    for b, (L, n) in enumerate(zip(lens, nodes)):
+        keep = torch.randint(0, n, (2,), generator=g).tolist()   # two drafts at most are seen
+        lo = L if W >= 0 else 0
+        seen = set()
+        for i in range(n):
+            m = sum(1 << j for j in keep) if i % 3 == 0 else 0
+            x["mask"][r + i] = m - (1 << 64) if m >> 63 else m
+            seen |= {L + j for j in keep if m >> j & 1}
+            if W >= 0:
+                lo = min(lo, max(0, int(x["pos"][r + i]) - W + 1))
+        seen |= set(range(lo, L))
+        for p in range(-(-(L + n) // page)):
+            if not any(s in seen for s in range(p * page, (p + 1) * page)):
+                x["table"][b, p] = -1 - p
+        r += n
+    O, lse, ws = call(csa, x, W=W)
+    assert csa.csa_check_status(ws) == 0 and check(x, O, lse, W=W).all()
