@@ -421,8 +421,9 @@ int csa_paged_append(const void* k, int64_t k_stride, const void* v, int64_t v_s
  *   O      [R, H, d] of element type o_dtype;  lse [R, H] float (nullable), as in
  *          csa_sparse_attn: partial results for csa_attn_combine, say with a
  *          csa_sparse_attn over compressed entries (both with CSA_F32 outputs)
- * A row that sees nothing gets O = 0, lse = -inf.  Rows outside every sequence are
- * left as they were.  Cache rows that no row of their sequence sees may hold
+ * A row that sees nothing gets O = 0, lse = -inf; a logit that is NaN or +infinity
+ * (from a query that is not finite) gives its (row, head) NaN, no other.  Rows
+ * outside every sequence are left as they were.  Cache rows that no row of their sequence sees may hold
  * anything, infinities and NaN included; those that some row sees hold finite
  * values.  The softmax weights are rounded to bf16 for the product with V (also
  * with an fp32 output); sums and statistics are fp32.

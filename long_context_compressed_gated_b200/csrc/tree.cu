@@ -139,6 +139,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return y;
 }
 
+// The larger one, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // Packed fp32 pairs (per component the scalar IEEE operation).
 __device__ __forceinline__ unsigned long long pair_bits(float2 a) {
   unsigned long long x;
@@ -917,15 +924,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(ex_full);
         if (!wait(ex_full, 1)) break;
         m_run = fmaxf(e0.x, e1.x);
-        f[0] = e0.y > 0.f ? fast_exp2(e0.x - m_run) : 0.f;
-        f[1] = e1.y > 0.f ? fast_exp2(e1.x - m_run) : 0.f;
+        f[0] = e0.y != 0.f ? fast_exp2(e0.x - m_run) : 0.f;
+        f[1] = e1.y != 0.f ? fast_exp2(e1.x - m_run) : 0.f;
         l = e0.y * f[0] + e1.y * f[1];
       }
       __syncwarp();
       tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      // l = 0: the row sees nothing; a query that is not finite makes it NaN, which goes on
+      const float inv = l != 0.f ? 1.f / l : 0.f;
       f[0] *= inv, f[1] *= inv;
-      const float lse2 = l > 0.f ? m_run + log2f(l) : -INFINITY;
+      const float lse2 = l != 0.f ? m_run + log2f(l) : -INFINITY;
       // rows of this warp, 32 channels at a time: scaled, staged in the shared memory of the
       // warp's own query rows (free now, and no other warp writes there; 16-byte pieces
       // swizzled by row), written out by whole rows
@@ -1073,7 +1081,7 @@ __global__ void __launch_bounds__(kMaxCtas, 4) tree_combine_kernel(const __grid_
       }
       float mn = m;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) mn = fmaxf(mn, ls[j]);
+      for (int j = 0; j < 8; ++j) mn = max_nan(mn, ls[j]);
       if (mn == -INFINITY) continue;  // no part has a key yet
       const float f = fast_exp2(m - mn);
       m = mn, l *= f;
@@ -1094,7 +1102,7 @@ __global__ void __launch_bounds__(kMaxCtas, 4) tree_combine_kernel(const __grid_
       __syncthreads();
       if (warp == 0) {
         float mn = m;
-        for (int p = 1; p < kWarps; ++p) mn = fmaxf(mn, s_ml[p].x);
+        for (int p = 1; p < kWarps; ++p) mn = max_nan(mn, s_ml[p].x);
         const float m_use = mn == -INFINITY ? 0.f : mn;
         const float f = fast_exp2(m - m_use);
         m = mn, l *= f;
@@ -1112,14 +1120,14 @@ __global__ void __launch_bounds__(kMaxCtas, 4) tree_combine_kernel(const __grid_
     }
     const int nh = w.z + row;  // (node, head) of the sequence's rows for this key head
     const int64_t orow = (int64_t)(w.x + nh / a.G) * a.H + w.y * a.G + nh % a.G;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
     for (int k = 0; k < C; ++k) {
       const int64_t to = orow * D + 32 * k + lane;
       if (a.o_f32) static_cast<float*>(a.O)[to] = acc[k] * inv;
       else static_cast<__nv_bfloat16*>(a.O)[to] = __float2bfloat16(acc[k] * inv);
     }
-    if (a.lse && lane == 0) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (a.lse && lane == 0) a.lse[orow] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
 }
 

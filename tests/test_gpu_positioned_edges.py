@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from tests import positioned_ref as ref
+from tests.test_gpu_tree import call, make
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -103,3 +104,29 @@ def test_append_keeps_infinities_where_they_are(csa, d, rot, style):
     a, b = k[..., :start], x[..., :start]
     assert torch.equal(a.nan_to_num(9, 8, 7), b.nan_to_num(9, 8, 7))
     assert torch.equal(ref.paged_rows(Vp.cpu(), table, 0, T).view(torch.int16), x.view(torch.int16))
+
+
+@pytest.mark.parametrize("lens,nodes,H,Hk,d,page", [
+    ([700], [1], 64, 1, 128, 64),                  # shared by several thread blocks, one row tile
+    ([20000, 3], [2, 2], 4, 1, 64, 64),            # many parts of few rows
+    ([3000, 800], [12, 30], 64, 1, 128, 64),       # two row tiles
+    ([40, 0, 90], [3, 2, 5], 8, 2, 64, 16)])       # within one block
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_queries_that_are_not_finite_show(csa, lens, nodes, H, Hk, d, page, out, value):
+    """NaN where such a query sees something, the empty result where it does not, and not a bit
+    changed anywhere else."""
+    x = make(lens, nodes, H, Hk, d, page, seed=50)
+    O, lse, _ = call(csa, x, out=out)
+    x["q"][0, H // 2, 5] = value
+    mid = (x["q"].shape[0] - 1) // 2
+    x["q"][mid, H - 1] = value
+    last = x["q"].shape[0] - 1
+    x["q"][last, 0, d - 1] = value
+    P, lp, ws = call(csa, x, out=out)
+    assert csa.csa_check_status(ws) == 0
+    bad = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+    bad[0, H // 2] = bad[mid, H - 1] = bad[last, 0] = True
+    bad &= lse != -math.inf
+    assert P[bad].isnan().all() and lp[bad].isnan().all()
+    assert torch.equal(P[~bad], O[~bad]) and torch.equal(lp[~bad], lse[~bad])
