@@ -364,8 +364,8 @@ int csa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_s
  *   dq, dk of x_dtype: token rows dq_stride / dk_stride elements apart (as q, k)
  *   dwq, dwk [d] f32 (written, not accumulated; the sums over all tokens and
  *          heads in a fixed order): given exactly when the side and its weight are
- * With T = 0 the weight gradients are zeros.  dq / dk must not overlap q, k, dyq
- * or dyk (CSA_ERR_INVALID_ARG), nor each other's elements.  Deterministic on one
+ * With T = 0 the weight gradients are zeros.  dq / dk must not overlap an input, dwq
+ * or dwk, nor these each other (CSA_ERR_INVALID_ARG); nor may dq and dk share elements.  Deterministic on one
  * GPU model (the split of the sums follows its SM count).  Workspace:
  * csa_qk_norm_rope_backward_workspace_bytes(). */
 size_t csa_qk_norm_rope_backward_workspace_bytes(int64_t T, int H, int Hk, int d);
@@ -390,6 +390,7 @@ int csa_qk_norm_rope_backward(const void* q, int64_t q_stride, const void* k, in
  *   pos    [T] int64 DEVICE: the position its key is rotated to (drafted tokens
  *          of one depth share a position but not a slot)
  *   wk, eps, inv_freq, rot_*: as csa_qk_norm_rope (wk NULL: no norm)
+ * The caches must not overlap an input or each other (CSA_ERR_INVALID_ARG).
  * Rows that no token names keep their bits.  The (sequence, slot) pairs of a call
  * are distinct.  A sequence, slot or page number outside its table is reported as
  * CSA_ERR_INDEX in the status word and its token skipped; nothing is read or
@@ -432,8 +433,8 @@ int csa_paged_append(const void* k, int64_t k_stride, const void* v, int64_t v_s
  * the rows of that sequence are unspecified.  All of it is read on the device in
  * stream order, so a captured call follows new lengths, tables and masks.
  * d in {64, 128}; page as csa_paged_append; H <= 1024, H % Hk == 0, any ratio;
- * B <= 65536; max_pages * page < 2^31 - 128; scale > 0; O must not overlap q
- * (CSA_ERR_INVALID_ARG).  Workspace: csa_tree_attn_workspace_bytes(); calls that can
+ * B <= 65536; max_pages * page < 2^31 - 128; scale > 0; O and lse must not overlap
+ * an input or each other (CSA_ERR_INVALID_ARG).  Workspace: csa_tree_attn_workspace_bytes(); calls that can
  * overlap on the GPU need one each. */
 size_t csa_tree_attn_workspace_bytes(int B, int64_t R, int H, int Hk, int d, int page, int max_pages);
 int csa_tree_attn(const void* q, const void* Kpages, const void* Vpages, const int32_t* block_table,

@@ -3,6 +3,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <initializer_list>
 
 #include "common.cuh"
 
@@ -52,6 +53,17 @@ inline size_t span(int64_t T, int64_t stride, int heads, int d, int dtype) {
 inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return an > 0 && bn > 0 && x < y + bn && y < x + an;
+}
+
+// A range of bytes, and whether one shares a byte with any of some others (null pointers share none).
+struct Bytes {
+  const void* p;
+  size_t n;
+};
+inline bool overlap_any(Bytes a, std::initializer_list<Bytes> others) {
+  for (const Bytes& b : others)
+    if (a.p != nullptr && b.p != nullptr && overlap(a.p, a.n, b.p, b.n)) return true;
+  return false;
 }
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }

@@ -121,8 +121,13 @@ extern "C" int csa_paged_append(const void* k, int64_t k_stride, const void* v, 
   if (n_pages > 0 && (rc = check_ptrs(Kpages, Vpages))) return rc;
   const size_t cache = (size_t)n_pages * Hk * page * d * 2;
   for (const void* c : {Kpages, Vpages})
-    if (overlap(c, cache, k, span(T, k_stride, Hk, d, CSA_BF16)) ||
-        overlap(c, cache, v, span(T, v_stride, Hk, d, CSA_BF16)))
+    if (overlap_any({c, cache}, {{k, span(T, k_stride, Hk, d, CSA_BF16)},
+                                 {v, span(T, v_stride, Hk, d, CSA_BF16)},
+                                 {wk, (size_t)d * 4},
+                                 {pos, (size_t)T * 8},
+                                 {slot, (size_t)T * 8},
+                                 {seq, (size_t)T * 4},
+                                 {block_table, (size_t)B * max_pages * 4}}))
       return CSA_ERR_INVALID_ARG;
   if (overlap(Kpages, cache, Vpages, cache)) return CSA_ERR_INVALID_ARG;
   AppendArgs a{};

@@ -426,7 +426,10 @@ int csa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_s
     a.side[i].y = out[i];
     a.side[i].blocks = heads[i] > 0 ? ceil_div(side_units(T, heads[i], d, wide), kThreads / (d / 8)) : 0;
   }
-  if (overlap(yq, span(T, (int64_t)H * d, H, d, y_dtype), yk, span(T, (int64_t)Hk * d, Hk, d, y_dtype)))
+  const Bytes outs[2] = {{yq, span(T, (int64_t)H * d, H, d, y_dtype)}, {yk, span(T, (int64_t)Hk * d, Hk, d, y_dtype)}};
+  const size_t wn = (size_t)d * 4, pn = (size_t)T * 8;
+  if (overlap_any(outs[0], {outs[1], {wq, wn}, {wk, wn}, {pos, pn}}) ||
+      overlap_any(outs[1], {{wq, wn}, {wk, wn}, {pos, pn}}))
     return CSA_ERR_INVALID_ARG;
   a.p.pos = pos;
   a.p.t0 = t0;
@@ -477,13 +480,18 @@ int csa_qk_norm_rope_backward(const void* q, int64_t q_stride, const void* k, in
     return e == cudaSuccess ? CSA_OK : cuda_fail(e);
   }
   if (H == 0 && Hk == 0) return CSA_OK;
+  // (dq and dk may lie between each other's rows, in one packed gradient)
+  const size_t wn = (size_t)d * 4;
+  if (overlap_any({dwq, wn}, {{dwk, wn}})) return CSA_ERR_INVALID_ARG;
   int64_t blocks[2];
   bwd_split(T, H, Hk, d, bytes_x, bytes_y, blocks);
   for (int i = 0; i < 2; ++i) {
     if (heads[i] == 0) continue;
     if ((rc = check_ptrs(dy[i], dx[i]))) return rc;
+    const size_t dn = span(T, dxs[i], heads[i], d, x_dtype);
+    if (overlap_any({dx[i], dn}, {{wq, wn}, {wk, wn}, {pos, (size_t)T * 8}, {dwq, wn}, {dwk, wn}}))
+      return CSA_ERR_INVALID_ARG;
     for (int j = 0; j < 2; ++j) {
-      const size_t dn = span(T, dxs[i], heads[i], d, x_dtype);
       if (overlap(dx[i], dn, a.side[j].x, span(T, a.side[j].x_stride, heads[j], d, x_dtype)) ||
           overlap(dx[i], dn, dy[j], span(T, (int64_t)heads[j] * d, heads[j], d, y_dtype)))
         return CSA_ERR_INVALID_ARG;

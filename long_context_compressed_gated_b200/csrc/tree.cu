@@ -1215,9 +1215,20 @@ int csa_tree_attn(const void* q, const void* Kpages, const void* Vpages, const i
   if (max_pages > 0 && (rc = check_ptrs(block_table))) return rc;
   if (n_pages > 0 && (rc = check_ptrs(Kpages, Vpages))) return rc;
   if ((rc = check_opt(lse))) return rc;
-  // a share writes its outputs while others still read the query rows
-  if (overlap(O, span(R, (int64_t)H * d, H, d, o_dtype), q, span(R, (int64_t)H * d, H, d, CSA_BF16)))
-    return CSA_ERR_INVALID_ARG;
+  // a share writes its outputs while others still read what all of them share
+  const size_t cache = (size_t)n_pages * Hk * page * d * 2;
+  const Bytes out{O, span(R, (int64_t)H * d, H, d, o_dtype)}, sums{lse, (size_t)R * H * 4};
+  for (const Bytes& o : {out, sums})
+    if (overlap_any(o, {{q, span(R, (int64_t)H * d, H, d, CSA_BF16)},
+                        {Kpages, cache},
+                        {Vpages, cache},
+                        {block_table, (size_t)B * max_pages * 4},
+                        {seq_lens, (size_t)B * 4},
+                        {q_start, (size_t)(B + 1) * 4},
+                        {mask, (size_t)R * 8},
+                        {W >= 0 ? pos : nullptr, (size_t)R * 8}}))
+      return CSA_ERR_INVALID_ARG;
+  if (overlap_any(out, {sums})) return CSA_ERR_INVALID_ARG;
   TreeArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.table = block_table;
