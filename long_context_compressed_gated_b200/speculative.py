@@ -23,8 +23,10 @@ def tree_verify_step(qkv, H, Hk, Kpages, Vpages, block_table, seq_lens, q_start,
     place; a later step commits the accepted rows by moving seq_lens (a chain's
     first rows stay where they are; rows of another branch are appended again to
     their final slots).  workspace: csa_tree_attn_workspace_bytes(), its status word
-    zeroed; pass one to read the status, which both kernels report to.  Returns
-    O [R, H, d]; lse [R, H] f32 receives the log-sum-exps when given."""
+    zeroed; pass one to read the status, which both kernels report to (without one a
+    number outside its table goes unseen).  Returns O [R, H, d]; lse [R, H] f32
+    receives the log-sum-exps when given.  An argument that only the attention
+    refuses raises after the rows have been appended: repeating the step is safe."""
     dev = _device(qkv, "qkv")
     n_pages, cached, page, d = _paged(Kpages, Vpages, dev)
     if qkv.dtype != torch.bfloat16:
@@ -33,8 +35,8 @@ def tree_verify_step(qkv, H, Hk, Kpages, Vpages, block_table, seq_lens, q_start,
         raise ValueError("qkv must be [R, %d] with dense rows, the cache's key heads %d" % ((H + 2 * Hk) * d, Hk))
     R, row = qkv.shape[0], qkv.stride(0) if qkv.shape[0] > 1 else qkv.shape[1]
     B, max_pages = _dense(block_table, torch.int32, 2, "block_table", dev)
-    if pos is None:
-        raise ValueError("pos must be given")
+    if pos is None or slot is None:  # (siblings share a position: it cannot stand in for their rows)
+        raise ValueError("pos and slot must be given")
     pp, slots = _vector(pos, R, torch.int64, "pos", dev), _vector(slot, R, torch.int64, "slot", dev)
     seqs, masks = _vector(seq, R, torch.int32, "seq", dev), _vector(mask, R, torch.int64, "mask", dev)
     lens = _vector(seq_lens, B, torch.int32, "seq_lens", dev)

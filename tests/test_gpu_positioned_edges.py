@@ -130,3 +130,21 @@ def test_queries_that_are_not_finite_show(csa, lens, nodes, H, Hk, d, page, out,
     bad &= lse != -math.inf
     assert P[bad].isnan().all() and lp[bad].isnan().all()
     assert torch.equal(P[~bad], O[~bad]) and torch.equal(lp[~bad], lse[~bad])
+
+
+def test_verification_step_wants_slots(csa):
+    """Two children of one node share a position: without slots they would share a cache row."""
+    from long_context_compressed_gated_b200.speculative import tree_verify_step
+    x = make([20], [3], 4, 2, 64, 16, seed=51)
+    c = {k: v.cuda() for k, v in x.items()}
+    c["pos"].copy_(torch.tensor([20, 21, 21]))
+    keep = c["Kp"].clone(), c["Vp"].clone()
+    good = dict(qkv=torch.randn(3, 8 * 64, device="cuda").to(BF), H=4, Hk=2, Kpages=c["Kp"], Vpages=c["Vp"],
+                block_table=c["table"], seq_lens=c["lens"], q_start=c["start"], mask=c["mask"],
+                seq=torch.zeros(3, dtype=torch.int32, device="cuda"), pos=c["pos"], inv_freq=csa.rope_inv_freq(64), scale=0.1)
+    with pytest.raises(ValueError):
+        tree_verify_step(slot=None, **good)
+    assert torch.equal(c["Kp"].view(torch.int16), keep[0].view(torch.int16))
+    tree_verify_step(slot=torch.tensor([20, 21, 22]).cuda(), **good)
+    rows = ref.paged_rows(c["Vp"].cpu(), x["table"], 0, 23)[20:]
+    assert torch.equal(rows, good["qkv"].cpu().view(3, 8, 64)[:, 6:])
