@@ -638,9 +638,13 @@ def csa_qk_norm_rope_backward(q, k, dyq, dyk, inv_freq, wq=None, wk=None, eps=1e
         else:
             if dw is None:
                 dw = torch.empty_like(w)
-                sides.append((dx, stride, dw, dw.data_ptr()))
+                dwp = dw.data_ptr()
             else:
-                sides.append((dx, stride, dw, _vector(dw, d, torch.float32, "dw", dev)))
+                dwp = _vector(dw, d, torch.float32, "dw", dev)
+            if heads == 0:  # the library leaves the side out
+                dw.zero_()
+                dwp = None
+            sides.append((dx, stride, dw, dwp))
     (dq, dqs, dwq, dwqp), (dk, dks, dwk, dwkp) = sides
     L = lib()
     ws = _scratch(workspace, dev, lambda: L.csa_qk_norm_rope_backward_workspace_bytes(T, H, Hk, d))

@@ -148,3 +148,17 @@ def test_verification_step_wants_slots(csa):
     tree_verify_step(slot=torch.tensor([20, 21, 22]).cuda(), **good)
     rows = ref.paged_rows(c["Vp"].cpu(), x["table"], 0, 23)[20:]
     assert torch.equal(rows, good["qkv"].cpu().view(3, 8, 64)[:, 6:])
+
+
+def test_sides_without_heads(csa):
+    """A side of no heads: no rows, and a weight whose gradient is the empty sum."""
+    f, w = csa.rope_inv_freq(64), torch.ones(64, device="cuda")
+    x, dy = (torch.randn(5, 2, 64, device="cuda") for _ in range(2))
+    none = x[:, :0].contiguous()
+    y = csa.csa_qk_norm_rope(x, none, f, wq=w, wk=w)
+    assert y[1].shape == (5, 0, 64)
+    want = csa.csa_qk_norm_rope_backward(x, None, dy, None, f, wq=w)
+    for given in (None, torch.full((64,), 3.0, device="cuda")):
+        got = csa.csa_qk_norm_rope_backward(x, none, dy, none, f, wq=w, wk=w, dwk=given)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2]) and got[1].shape == (5, 0, 64)
+        assert (got[3] == 0).all() and (given is None or got[3] is given)
