@@ -583,7 +583,8 @@ def csa_qk_norm_rope(q, k, inv_freq, wq=None, wk=None, eps=1e-6, pos=None, t0=0,
     packed projection are fine; either may be None).  inv_freq [rot/2] float64 on
     the CPU (None: no rotation), turning channels rot_start .. rot_start + rot.
     pos [T] int64 positions on the device, or None: t0, t0 + 1, ...
-    Returns (yq, yk) of out_dtype (default: the inputs' type)."""
+    Returns (yq, yk) of out_dtype (default: the inputs' type), which autograd does
+    not follow: gradients come from csa_qk_norm_rope_backward."""
     dev, dtype, T, H, Hk, d, qs, ks = _qk_sides(q, k)
     ot = dtype if out_dtype is None else out_dtype
     wqp, wkp = _vector(wq, d, torch.float32, "wq", dev), _vector(wk, d, torch.float32, "wk", dev)

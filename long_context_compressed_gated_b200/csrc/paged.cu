@@ -10,8 +10,10 @@
 // the chain seq, slot -> table -> store for single tokens.  A group of d/8 lanes
 // takes one token's chunk of key heads: the page number and the rotation are
 // found once per chunk, and K and V rows are loaded before either is needed.  28.9 k
-// tokens of 8 key heads of 128 (237 MB): 45 us, 5.3 TB/s; with 4 heads a group 49 us, with
-// 2 heads 61; four rows ahead instead of two 55.
+// tokens of 8 key heads of 128 (237 MB): 44 us, 5.3 TB/s; with 4 heads a group 49 us, with
+// 2 heads 61; four rows ahead instead of two 55.  Four blocks an SM leave 64 registers a thread,
+// of which the rotation in halves spills 36 bytes, in pairs 12.  200 k tokens of one key head
+// (205 MB): 70 us, 2.9 TB/s: a token's angles then serve one row and the instructions bound it.
 #include "checks.cuh"
 #include "rope.cuh"
 

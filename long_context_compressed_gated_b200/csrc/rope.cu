@@ -11,7 +11,7 @@
 // writes dx.  A group of d/8 lanes takes one token's chunk of heads, so the
 // rotation's coefficients are built once per chunk; to keep enough bytes in flight
 // the forward loads kAhead rows before it uses one (32768 tokens of 65 heads of 128,
-// bf16, 1.09 GB: 173 us, 6.3 TB/s), the backward has rows on their way in shared memory
+// bf16, 1.09 GB: 170-175 us, 6.2-6.4 TB/s), the backward has rows on their way in shared memory
 // (half the tokens, 0.82 GB: 127 us, 6.4 TB/s, then the sum of dw).
 #include <cmath>
 
@@ -51,16 +51,17 @@ constexpr int kAhead = 4;          // rows of a group loaded before the first is
 constexpr int fwd_blocks_per_sm(int bytes_x) { return bytes_x == 4 ? 3 : 4; }
 // Backward: blocks per SM and rows of a group on their way, by element sizes.  600 MB of 65
 // heads of 128 with the sum of dw (the bytes alone take 92 us): bf16 five and three 101 us (two
-// 106, four 102; six and three 117); fp32 four and four 97 (three 105, five blocks 124); fp32
-// gradients of bf16 four and four 95 (five blocks 106); bf16 gradients of fp32 five and five
-// 106 (four ahead 115, four blocks 114).
+// 106, four 102; six and three 117); fp32 four and four 96 (three 105, five blocks 124; 121 in
+// pairs); fp32 gradients of bf16 four and four 93 (five blocks 106); bf16 gradients of fp32 five
+// and five 106 (four ahead 115, four blocks 114).
 constexpr int kBwdThreads = 128;
 constexpr int bwd_blocks_per_sm(int bytes_y) { return bytes_y == 4 ? 4 : 5; }
 constexpr int bwd_ahead(int bytes_x, int bytes_y) { return bytes_y == 4 ? 4 : bytes_x == 4 ? 5 : 3; }
 constexpr bool bwd_wide(int bytes_x, int bytes_y) { return bytes_x + bytes_y > 4; }
 // Most heads of one token that share a set of coefficients: fewer sets with 16, shorter pieces
-// of memory with 8.  Forward, 600 MB: bf16 outputs 102 against 115 us with 8, fp32 outputs
-// 98 against 94; backward: bf16 118 against 128, with an fp32 side 106 against 100.
+// of memory with 8.  Forward: bf16 outputs 173 us with 16, 192 with 8 (1.09 GB), fp32 outputs 99
+// and 97 (of bf16, 600 MB), 118 and 107 (of fp32, pairs); backward, 600 MB: bf16 101 and 106
+// (all channels in halves 109 and 120), fp32 126 and 121 (pairs), bf16 gradients of fp32 113 and 111.
 constexpr int head_chunk_most(bool wide) { return wide ? 8 : 16; }
 // What a unit costs beside its rows (its token's coefficients, the first loads), in rows.
 constexpr int kUnitRows = 2;
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, fwd_blocks_per_sm(sizeof(TX))) norm_
 // of dw in registers, and the block adds its groups' shares in order: one partial
 // row per block, summed in order by norm_rope_dw_kernel (no atomics).  Rows wait in
 // shared memory, not in registers: the bytes in flight are what bounds it (rows in
-// registers: 117 us where this takes 101, 16384 tokens of 65 heads 149 and 136).
+// registers: 117 us where this takes 101, 16384 tokens of 65 heads 149 and 141).
 template <int D, typename TX, typename TY, int STYLE>
 __global__ void __launch_bounds__(kBwdThreads, bwd_blocks_per_sm(sizeof(TY)))
     norm_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {

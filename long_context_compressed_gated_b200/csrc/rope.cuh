@@ -46,7 +46,7 @@ bool rope_params(const double* inv_freq, int rot, RopeParams& p);
 // Heads of one token that a lane group takes: `most`, halved while the groups would leave
 // an SM under 384 threads (a decode step of 16 tokens x 64 heads: 2 heads, 3.6 us; with 16
 // heads 6.8).  The coefficients are built once per group, so long calls keep `most` (32768
-// tokens of 65 heads, bf16: 174 us with 16, 196 with 8).
+// tokens of 65 heads, bf16: 173 us with 16, 192 with 8).
 int rope_head_chunk(int64_t T, int heads, int d, int most);
 
 __device__ __forceinline__ float4 ld_f4(const float* p) { return *reinterpret_cast<const float4*>(p); }

@@ -42,7 +42,7 @@
 // heads of 128 on one key head (807 MB): HBM, 139 us, 5.8 TB/s (6.3 while streaming).  Trees of
 // 8 .. 16 nodes over 21 k .. 33 k rows, the same heads: the softmax of 128 x 128 logits, 1024
 // clocks of the SFU at least, beside 1024 clocks of products; 1.9 us for a pair of row tiles,
-// 165 us (186 under the power cap), 0.96 PFLOP/s.  32 heads of 64 on 8 key heads, window 4096:
+// 165 us and 0.96 PFLOP/s, 180 .. 197 us and 0.80 .. 0.88 under the power cap.  32 heads of 64 on 8 key heads, window 4096:
 // the chain from S over the softmax to PV, 1.0 us a tile, and 3 .. 4 us to change segments; 64 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -68,17 +68,19 @@ constexpr int kTile = 128;          // rows of a tensor tile, keys of a key tile
 constexpr int kItemRows = 2 * kTile;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kLoadWarp2 = 10;
-constexpr int kThreads = 352;       // 11 warps, up to 168 registers a thread
+constexpr int kThreads = 352;       // 11 warps, up to 168 registers a thread (d = 64 spills 8 bytes)
 constexpr int kMaxNodes = 64;       // bits of a mask
 constexpr int kMaxSeqs = 65536;     // every CTA adds up all sequences' tiles, within the bound of the other roles' waits
 // Lengths on the line of all items' key tiles, in key tiles of a single row tile (1.0 us;
-// a pair of row tiles takes 2.07 us): a tile of a single row tile, of a pair, and what
+// a pair of row tiles takes 1.9 us): a tile of a single row tile, of a pair, and what
 // starting an item costs beside them (the outputs before it written, query rows read,
 // the pipeline filled).
 constexpr int kSingleCost = 1, kPairCost = 2, kItemCost = 6;
-// A CTA's share at least.  Fewer, longer shares save the merge of partial results where
-// all fit one CTA; beyond that more CTAs win (8 sequences of 1 k .. 8 k rows, 8 drafts
-// each: 41 us with 12 more, 37 with 4 more, 36 with 2 more).
+// A CTA's share at least: an item's cost and three key tiles.  Fewer, longer shares save the
+// merge of partial results where all fit one CTA; beyond that more CTAs win (verification step
+// of 8 sequences of 1 k .. 8 k rows, 8 drafts each: 39.4 us with twelve key tiles, 36.4 with six,
+// 35.2 with four, 34.5 with three, 35.3 with two; 15 sequences of 500 rows: 23.0, 20.7, 19.3,
+// 18.3, 16.7).
 constexpr int kMinShare = kItemCost + 3 * kSingleCost;
 constexpr float kRescaleSlack = 8.0f;  // raise the running max only when it grows by > 2^8
 constexpr float kLn2 = 0.69314718055994531f;
@@ -534,9 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       return q;
     };
     int n = 0;  // segments published
-    bool live = true;
 #pragma unroll 1
-    for (int64_t g = first; g < last && live;) {
+    for (int64_t g = first; g < last;) {
       Seq q = sequence(b);
       while (g >= at + q.total(a.Hk) && b + 1 < a.B) {
         at += q.total(a.Hk);
@@ -601,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) a.split[2 * c] = split;
     // no more segments
-    if (live && (n < 2 || wait(&seg_free[n & 1], (uint32_t)((n / 2 - 1) & 1))) && lane == 0) {
+    if ((n < 2 || wait(&seg_free[n & 1], (uint32_t)((n / 2 - 1) & 1))) && lane == 0) {
       reinterpret_cast<Segment*>(s_seg + (n & 1) * 128)->valid = 0;
       mbar_arrive(&seg_full[n & 1]);
     }
@@ -1019,8 +1020,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   slots of CTAs c+1, c+2, ..
 // O = sum_i 2^(lse_i - lse) O_i with lse = log2 sum_i 2^lse_i, in the parts' order.
 // Latency bound: a block finds the rows of all items from one read of the records;
-// a warp takes a row and loads eight parts' log-sum-exps and outputs at once.  With
-// fewer rows than blocks the eight warps of a block share the parts of one row.
+// a warp takes a row and loads eight parts' log-sum-exps and outputs at once (d = 128 spills 84
+// bytes of the 64 registers a thread that four blocks an SM leave).  With fewer rows than blocks
+// the eight warps of a block share the parts of one row.
 constexpr int kMaxCtas = 256;
 
 template <int D>
